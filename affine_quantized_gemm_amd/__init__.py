@@ -36,6 +36,9 @@ EXPORTS = (
     "qmm_small_m_ws", "qmm_small_m_workspace_bytes", "qmm_small_m_split_forced", "qmm_split_plan",
     "qmm_small_m_batched", "qmm_small_m_nt", "qmm_small_m_nt_ws", "qmm_small_m_nt_workspace_bytes",
     "qmm_build_digest", "qmm_small_m_noalloc", "qmm_probe_small_m_loop",
+    "qmm_kv_record_bytes", "qmm_kv_append", "qmm_kv_read", "qmm_kv_attend", "qmm_kv_attend_workspace_bytes",
+    "qmm_kv_pages_workspace_bytes", "qmm_kv_copy_pages", "qmm_kv_reserve", "qmm_kv_fork", "qmm_kv_free",
+    "qmm_kv_compact",
 )
 NOALLOC_SCRATCH_BYTES = 8 * 1024 * 1024  # QMM_NOALLOC_SCRATCH_BYTES
 
@@ -88,6 +91,18 @@ def _load():
         "qmm_small_m_noalloc": (i32, [i32, i32, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp]),
         "qmm_probe_small_m_loop": (i32, [i32, i32, i32, i64, i64, i64, vp, ctypes.POINTER(vp), ctypes.POINTER(vp),
                                          ctypes.POINTER(vp), vp, i32, i32, vp]),
+        "qmm_kv_record_bytes": (i64, [vp]),
+        "qmm_kv_append": (i32, [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, i64, i64, vp, i64, i64, vp]),
+        "qmm_kv_read": (i32, [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, vp, vp]),
+        "qmm_kv_attend_workspace_bytes": (i64, [vp, i64, i64, i64, i64, i64]),
+        "qmm_kv_attend": (i32, [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, i64, i64, i64, ctypes.c_float, vp, vp, vp,
+                                i64, vp, i64, vp]),
+        "qmm_kv_pages_workspace_bytes": (i64, [vp, i64]),
+        "qmm_kv_copy_pages": (i32, [vp, vp, vp, i64, vp]),
+        "qmm_kv_reserve": (i32, [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp]),
+        "qmm_kv_fork": (i32, [vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, i64, vp]),
+        "qmm_kv_free": (i32, [vp, i64, vp, i64, vp, vp, vp, i64, vp]),
+        "qmm_kv_compact": (i32, [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -466,3 +481,6 @@ def small_m_noalloc(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor, bia
                                scales.data_ptr(), biases.data_ptr(), out.data_ptr(), _stream(stream)),
            "qmm_small_m_noalloc")
     return out
+
+
+from .kv import KVCache, record_words  # noqa: E402,F401  (needs the definitions above)

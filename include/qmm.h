@@ -329,6 +329,168 @@ int qmm_probe_small_m_loop(int dt, int bits, int group_size, int64_t M, int64_t 
                            const uint32_t* const* wq, const void* const* scales, const void* const* biases, void* y,
                            int count, int passes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged K/V cache held in 4 bits, and attention over it.
+ *
+ * What a decoder keeps next to the products above: the keys and values of
+ * the tokens so far, quantized with qmm_quantize's rule at 4 bits (one scale
+ * and one bias of dtype dt per token, kv head and group of group_size
+ * consecutive values), in pages of page_size tokens.
+ *
+ * The pool is one dense array [layers][pages][kv_heads] of records, one
+ * record of page_size * (head_dim + 8 * head_dim / group_size) bytes per page
+ * of one layer and head.  With PS = page_size, D = head_dim, G = D / gs, a
+ * record holds in this order (words are uint32):
+ *   K codes  [PS][4][D/32] words        word (t, j, s): values d = 32 s + 8 j
+ *            + e of token t, value e in bits 4e..4e+3 (a row's 16-byte pieces
+ *            are the matrix-core operand of one lane)
+ *   V codes  [PS/4][16][2][D/64] words  word (u, i, p, c): token 4u + 2p in
+ *            the low half, 4u + 2p + 1 in the high half, each with the values
+ *            d = 64 c + 16 n + i in bits 4n..4n+3, n = 0..3
+ *   K s, b   [PS/4][G][2][4] values     (u, g): the scales of tokens
+ *            4u..4u+3, then their biases
+ *   V s, b   the same
+ *
+ * Sequences: `tables` [seqs][table_width] (int32, dense) names the pages of
+ * each sequence in order, entries not in use negative; `lens` [seqs] (int32)
+ * is its length in tokens.  Position t of sequence b lies in slot
+ * t % PS of page tables[b][t / PS].  `refs` [pages] (int32) counts the
+ * sequences that hold each page (0: free).  Tables, lengths and counts live
+ * in device memory and are read when the kernels run, so that steps can be
+ * captured in a graph.
+ *
+ * New tokens of a call: `rows` in all, dense over the sequences.  With
+ * starts == NULL every sequence has max_new of them (rows = seqs * max_new);
+ * else starts [seqs + 1] (int32, device) are the first rows of the
+ * sequences, at most max_new each.  lens counts them in: row i of sequence b
+ * with n new tokens is position lens[b] - n + i.
+ *
+ * Every page id, length, start and sequence number read from device memory
+ * is checked against the sizes given here before it becomes an address: a
+ * position whose table entry names no page of the pool, or that lies outside
+ * the table, is skipped by qmm_kv_append, reads as zeros from qmm_kv_read and
+ * is not attended to.
+ * ------------------------------------------------------------------------- */
+typedef struct qmm_kv_cache {
+    int32_t dt;          /* qmm_dtype of scales, biases, q, k, v and outputs */
+    int32_t group_size;  /* 32, 64 or 128, at most head_dim */
+    int32_t head_dim;    /* 64, 128 or 256 */
+    int32_t kv_heads;    /* 1..65535 */
+    int32_t page_size;   /* 32, 64, 128 or 256 tokens */
+    int32_t layers;      /* 1..65535 */
+    int64_t pages;       /* 0..2^30 */
+    void* pool;          /* 16-byte aligned device memory */
+} qmm_kv_cache;
+
+/* Bytes of one record, or a negative status for an unsupported geometry
+ * (pool is not looked at).  A pool takes layers * pages * kv_heads records. */
+int64_t qmm_kv_record_bytes(const qmm_kv_cache* cache);
+
+/*
+ * Quantize the new tokens' keys and values into `layer` of the cache.
+ * k, v: dt, element (row, head, d) at row * stride_row + head * stride_head
+ * + d; base 16-byte aligned, strides (in elements, >= 0) multiples of 8.
+ * Bit-exact: the codes, scales and biases are qmm_quantize's.  Other tokens'
+ * slots of the same pages are not touched.
+ */
+int qmm_kv_append(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_new, int64_t rows,
+                  const int32_t* tables, int64_t table_width, const int32_t* lens, const int32_t* starts,
+                  const void* k, int64_t k_stride_row, int64_t k_stride_head,
+                  const void* v, int64_t v_stride_row, int64_t v_stride_head, void* stream);
+
+/*
+ * Dequantize the new tokens' (the last n of each sequence) keys and values
+ * out of `layer`: k, v [rows][kv_heads][head_dim] (dense), RNE_dt(s*q + b) as
+ * qmm_dequantize.  The whole of a sequence: all its tokens as new ones.
+ */
+int qmm_kv_read(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_new, int64_t rows,
+                const int32_t* tables, int64_t table_width, const int32_t* lens, const int32_t* starts,
+                void* k, void* v, void* stream);
+
+/*
+ * Attention of the new tokens over `layer` of the cache (which already holds
+ * them): out [rows][heads][head_dim] (dt, dense) and, unless NULL, lse
+ * [rows][heads] (fp32, natural logarithm of the sum of exponentials).
+ *   - heads is a multiple of kv_heads; heads h*heads/kv_heads .. share kv
+ *     head h.  1 <= max_new <= 64.
+ *   - q as k in qmm_kv_append.  Scores are scale * q . k_hat.
+ *   - A row sees every token before its sequence's new ones, and of these
+ *     the ones up to itself; with mask (int64 [rows], device) instead the
+ *     new tokens j whose bit j is set in the row's word (a draft tree: the
+ *     row's own token and its ancestors).
+ *   - A row that sees nothing gives zeros and lse = -infinity.
+ * fp32 accumulation, softmax and sums; k_hat and v_hat are not rounded; the
+ * probabilities (times the scale of their value) are rounded to dt for the
+ * second product; one rounding to dt at the end.  Deterministic.
+ *
+ * max_len: no sequence is longer (1..table_width * page_size); it sets how
+ * the tokens are split over workgroups.  Longer ones are still attended to
+ * in whole, with the last part longer than planned.
+ * workspace: device memory of at least qmm_kv_attend_workspace_bytes(...)
+ * bytes, 16-byte aligned (may be NULL when that is 0), not aliasing the
+ * other arrays; two calls in flight need two.
+ * heads < 1, or not a multiple of kv_heads, max_new > 64 ->
+ * QMM_ERR_UNSUPPORTED.
+ */
+int64_t qmm_kv_attend_workspace_bytes(const qmm_kv_cache* cache, int64_t seqs, int64_t max_new, int64_t rows,
+                                      int64_t heads, int64_t max_len);
+int qmm_kv_attend(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_new, int64_t rows,
+                  const int32_t* tables, int64_t table_width, const int32_t* lens, const int32_t* starts,
+                  const void* q, int64_t q_stride_row, int64_t q_stride_head, int64_t heads, float scale,
+                  const int64_t* mask, void* out, float* lse, int64_t max_len,
+                  void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Pages.  All layers move together; ids out of range are skipped.
+ *
+ * qmm_kv_copy_pages: page dst[i] <- page src[i] for i < n (device int32
+ * arrays).  No page may be both a source and a destination, or twice a
+ * destination.
+ *
+ * The next ones keep the bookkeeping.  A sequence holds the pages its row
+ * names; `lens` may be cut back by the caller (rejected drafts) as long as
+ * no token of a page shared with a fork is written again.
+ *
+ * qmm_kv_reserve: room for add[s] more tokens of every sequence s < seqs
+ * (device int32): missing pages are taken, lens[s] += add[s], ok[s] = 1.
+ * A sequence whose pages are not there (or whose row is too short, or
+ * add[s] < 0) keeps what it has, ok[s] = 0.
+ *
+ * qmm_kv_fork: sequence dst[i] becomes a copy of sequence src[i], i < n: it
+ * shares the whole pages (refs + 1) and gets a page of its own with a copy
+ * of a partly filled last one, in every layer.  dst[i] must hold nothing; no
+ * dst may be a src or named twice.  ok[i] = 1, or 0 (and an empty dst) where
+ * no page is left or src[i] is not a sound sequence.
+ *
+ * Both take the free pages lowest first and serve the requests in order: one
+ * gets its pages if the free ones suffice for it and all before it.
+ *
+ * qmm_kv_free: every page that the named sequences hold is given up
+ * (refs - 1), their rows are cleared to -1 and their lengths to 0.
+ *
+ * qmm_kv_compact: the live pages (refs > 0; L of them) move into ids
+ * 0..L-1: those at or above L, in order, into the free ones below L, in
+ * order.  tables_out and refs_out get tables and refs rewritten for that
+ * (they may be tables and refs themselves), live_out[0] = L.  The contents of
+ * pages at or above L stay.
+ *
+ * workspace: qmm_kv_pages_workspace_bytes(cache, n) bytes of device memory,
+ * 16-byte aligned, for reserve (n = seqs), fork (n) and compact (n = 0).
+ */
+int64_t qmm_kv_pages_workspace_bytes(const qmm_kv_cache* cache, int64_t n);
+int qmm_kv_copy_pages(const qmm_kv_cache* cache, const int32_t* src, const int32_t* dst, int64_t n, void* stream);
+int qmm_kv_reserve(const qmm_kv_cache* cache, int64_t seqs, int32_t* tables, int64_t table_width, int32_t* lens,
+                   int32_t* refs, const int32_t* add, int32_t* ok, void* workspace, int64_t workspace_bytes,
+                   void* stream);
+int qmm_kv_fork(const qmm_kv_cache* cache, int64_t seqs, int32_t* tables, int64_t table_width, int32_t* lens,
+                int32_t* refs, const int32_t* src, const int32_t* dst, int64_t n, int32_t* ok, void* workspace,
+                int64_t workspace_bytes, void* stream);
+int qmm_kv_free(const qmm_kv_cache* cache, int64_t seqs, int32_t* tables, int64_t table_width, int32_t* lens,
+                int32_t* refs, const int32_t* which, int64_t n, void* stream);
+int qmm_kv_compact(const qmm_kv_cache* cache, int64_t seqs, const int32_t* tables, int64_t table_width,
+                   const int32_t* refs, int32_t* tables_out, int32_t* refs_out, int32_t* live_out, void* workspace,
+                   int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
