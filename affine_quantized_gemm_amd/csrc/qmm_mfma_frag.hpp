@@ -303,6 +303,40 @@ struct DtBits<DT_BF16> {
     }
 };
 
+// One direct global-to-LDS load: 16 bytes per active lane, lane q to
+// lds_dst + 16 q, non-temporal.  Written as assembly on purpose: for a
+// global-to-LDS load the compiler knows of, it waits for every such load
+// before any later LDS read, which would drain the prefetch ring each tile.
+// Callers wait explicitly (s_waitcnt vmcnt, in-order retirement).  M0 (the
+// LDS address) is used by nothing else in these kernels.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// base: a 64-bit address, the same in every lane (moved to scalar
+// registers here); voff: this lane's byte offset from it; m0: the LDS byte
+// address of lane 0's 16 bytes (the same in every lane).
+//
+// NT: non-temporal (each weight line is read once).  Without it (row-block
+// grids) L2 keeps the line for the other row blocks of the same column slot.
+template <bool NT = true>
+__device__ __forceinline__ void dma16(const void* base, uint32_t voff, uint32_t m0) {
+    // (readfirstlane returns a signed int: each half goes through uint32_t so
+    // that widening cannot sign-extend the low word over the high one)
+    const uint64_t b = reinterpret_cast<uintptr_t>(base);
+    const uint32_t lo = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b)));
+    const uint32_t hi = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b >> 32)));
+    const uint64_t sb = (static_cast<uint64_t>(hi) << 32) | lo;
+    if constexpr (NT)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt"
+                     :
+                     : "s"(__builtin_amdgcn_readfirstlane(m0)), "v"(voff), "s"(sb)
+                     : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                     :
+                     : "s"(__builtin_amdgcn_readfirstlane(m0)), "v"(voff), "s"(sb)
+                     : "memory", "m0");
+}
+#pragma clang diagnostic pop
 
 }  // namespace mf
 }  // namespace qmm

@@ -81,9 +81,15 @@ def test_attend_refusals(kw, status):
     assert attend(**kw) == status
 
 
-def test_attend_workspace_sizes():
+def test_attend_workspace_refusals():
     g = geo(pages=9)
-    assert L.qmm_kv_attend_workspace_bytes(g, 0, 3, 0, 32, 1 << 17) == 0
+    long = 1 << 17
+    need = L.qmm_kv_attend_workspace_bytes(g, 2, 3, 6, 32, long)
+    assert need > 0 and need % 16 == 0
+    assert attend(g=g, max_len=long, ws=None) == INV
+    assert attend(g=g, max_len=long, bytes=need - 1) == INV
+    assert attend(g=g, max_len=long, ws=MIS8) == MIS
+    assert L.qmm_kv_attend_workspace_bytes(g, 0, 3, 0, 32, long) == 0
     assert L.qmm_kv_attend_workspace_bytes(g, 2, 3, 6, 32, 0) == INV
     assert L.qmm_kv_attend_workspace_bytes(g, 2, 3, 6, 33, 5) == UNS
     assert L.qmm_kv_attend_workspace_bytes(g, 2, 65, 130, 32, 5) == UNS
