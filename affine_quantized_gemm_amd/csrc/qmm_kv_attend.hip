@@ -1,4 +1,5 @@
 // Attention over the paged 4-bit K/V cache: how a call is cut, and its launch.
+#include <cstdlib>
 #include "qmm_kv_attend.hpp"
 
 namespace qmm {
@@ -14,23 +15,29 @@ template <> AttendFn attend_fn<DT_BF16, 256>(int, int);
 namespace {
 
 struct AttendPlan {
-    int row_tiles, row_groups, splits, chunk;
+    int row_tiles, row_groups, parts;
+    int64_t bytes;
 };
 
-// Tokens are split until the workgroups fill the chip (two for each of 256
-// CUs), in parts of 128 tokens (a step for each wavefront) at least.
+// Parts for kWorkgroups workgroups over the kv heads and row groups; where
+// the sequences are that many, or short, or too many to plan, one part each.
+constexpr int kWorkgroups = 512;
+static_assert(4 * kWorkgroups <= QMM_KV_ATTEND_ZEROED_BYTES, "a counter for every (sequence, row group, head)");
+
 AttendPlan plan_of(const qmm_kv_cache& c, int64_t seqs, int64_t max_new, int64_t heads, int64_t max_len) {
     AttendPlan p;
     const int64_t rows = max_new * (heads / c.kv_heads);
     p.row_tiles = rows <= 16 ? 1 : 2;
     p.row_groups = static_cast<int>((rows + 16 * p.row_tiles - 1) / (16 * p.row_tiles));
-    const int64_t units = seqs * c.kv_heads * p.row_groups;
-    int64_t splits = (512 + units - 1) / units;
-    const int64_t most = (max_len + 127) / 128;
-    splits = splits < most ? splits : most;
-    const int64_t chunk = ((max_len + splits - 1) / splits + 127) / 128 * 128;
-    p.splits = static_cast<int>((max_len + chunk - 1) / chunk);
-    p.chunk = static_cast<int>(chunk < INT32_MAX / 2 ? chunk : INT32_MAX / 2);
+    const int64_t each = static_cast<int64_t>(c.kv_heads) * p.row_groups;
+    static const int tgt = getenv("KV_TARGET") ? atoi(getenv("KV_TARGET")) : kWorkgroups;
+    int64_t parts = tgt / each;
+    const int64_t most = seqs * ((max_len + kChunk - 1) / kChunk);
+    parts = parts < most ? parts : most;
+    if (parts <= seqs || seqs > 64 * kPlanLanes) parts = seqs;
+    p.parts = static_cast<int>(parts);
+    // (sequences are cut only where seqs * each < kWorkgroups: the counters fit their fixed place)
+    p.bytes = parts > seqs ? QMM_KV_ATTEND_ZEROED_BYTES + parts * each * part_floats(c.head_dim, p.row_tiles) * 4 : 0;
     return p;
 }
 
@@ -38,9 +45,7 @@ AttendPlan plan_of(const qmm_kv_cache& c, int64_t seqs, int64_t max_new, int64_t
 
 int64_t attend_workspace(const qmm_kv_cache& c, int64_t seqs, int64_t max_new, int64_t, int64_t heads,
                          int64_t max_len) {
-    const AttendPlan p = plan_of(c, seqs, max_new, heads, max_len);
-    if (p.splits == 1) return 0;
-    return (seqs * max_new * heads * p.splits * (c.head_dim + 2) * 4 + 15) / 16 * 16;
+    return plan_of(c, seqs, max_new, heads, max_len).bytes;
 }
 
 hipError_t launch_attend(const qmm_kv_cache& c, const AttendArgs& a) {
@@ -52,17 +57,16 @@ hipError_t launch_attend(const qmm_kv_cache& c, const AttendArgs& a) {
     k.q_head = a.q.stride_head;
     k.heads = a.heads;
     k.group = a.heads / c.kv_heads;
-    k.row_groups = p.row_groups;
-    k.splits = p.splits;
-    k.chunk = p.chunk;
+    k.parts = p.parts;
     k.scale = a.scale;
     k.mask = a.mask;
     k.out = static_cast<uint16_t*>(a.out);
     k.lse = a.lse;
-    k.part = static_cast<float*>(a.workspace);
-    const int64_t units = static_cast<int64_t>(a.s.seqs) * c.kv_heads * p.splits;
-    const int64_t blocks = (units + 7) / 8 * 8 * p.row_groups;
-    if (blocks > INT32_MAX || static_cast<int64_t>(a.s.seqs) * a.s.max_new * a.heads > INT32_MAX) return hipErrorInvalidValue;
+    k.done = static_cast<uint32_t*>(a.workspace);
+    k.sums = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + QMM_KV_ATTEND_ZEROED_BYTES);
+    const int64_t blocks = (static_cast<int64_t>(p.parts) * c.kv_heads + 7) / 8 * 8;
+    if (blocks > INT32_MAX || p.row_groups > 65535) return hipErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(p.row_groups));
     AttendFn fn = nullptr;
     const bool half = c.dt == QMM_F16;
     switch (c.head_dim) {
@@ -71,7 +75,7 @@ hipError_t launch_attend(const qmm_kv_cache& c, const AttendArgs& a) {
         case 256: fn = half ? attend_fn<DT_F16, 256>(c.group_size, p.row_tiles) : attend_fn<DT_BF16, 256>(c.group_size, p.row_tiles); break;
         default: break;
     }
-    return fn != nullptr ? fn(k, blocks, a.stream) : hipErrorInvalidValue;
+    return fn != nullptr ? fn(k, grid, a.stream) : hipErrorInvalidValue;
 }
 
 }  // namespace kv

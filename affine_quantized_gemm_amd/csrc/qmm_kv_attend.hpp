@@ -7,10 +7,13 @@
 // per token and group; with p = 2^(S - R),
 //   O[row, d] = sum_t (p s_V[t, g]) (c[t, d] - 8)  +  sum_t p (b_V[t, g] + 8 s_V[t, g])
 // takes the second product's operand P' = p s_V, one per group, to codes
-// again.  Nothing is ever dequantized.  The codes are centred because P' is
+// again.  Nothing is ever dequantized, and what remains besides the codes --
+// biases of K against sums of q, sums of p b and p s -- are small products
+// of the stored scales and biases as they are, on the matrix cores as well:
+// the vector ALUs bound this kernel.  The codes are centred because P' is
 // rounded to 11 bits: its error is then weighed by |c - 8|, about the size of
 // the values, and not by c; the centring itself is -8 sum_t P', a product
-// with ones on the matrix core.  R = M + E is a running reference: M follows
+// with ones.  R = M + E is a running reference: M follows
 // the scores' maximum and E the exponent of the largest s_V, so that P' stays
 // near 1 whatever the values' size.  Both are moved (and everything summed so
 // far scaled) only when a score passes M by 8, or a scale 2^E by 2^7.
@@ -37,6 +40,8 @@
 // word, so that a masked word is two k-slots.
 #pragma once
 
+#include <type_traits>
+
 #include "qmm_device.hpp"
 #include "qmm_internal.hpp"
 #include "qmm_kv.hpp"
@@ -52,38 +57,29 @@ constexpr float kFar = -3.0e38f;
 // Wavefronts a SIMD that the registers are to leave room for.
 constexpr int attend_occupancy(int dim, int row_tiles) { return dim == 256 ? 1 : row_tiles == 1 ? 3 : 2; }
 
+// The tokens of a sequence are cut into parts of whole chunks, one workgroup
+// a part.
+constexpr int kChunk = 32 * kAttendWaves;
+constexpr int kPlanLanes = 4;  // sequences a lane holds while the cut is planned: up to 256 are cut
+
 struct AttendParams {
     Seqs s;
     const uint16_t* q;
     int64_t q_row, q_head;
-    int heads, group;       // heads of one kv head
-    int row_groups;         // row tiles a sequence needs at most / RT
-    int splits;             // parts a sequence is cut into at most
-    int chunk;              // tokens a part (a multiple of 32), more where the sequence is longer than planned
+    int heads;
+    uint32_t group;         // heads of one kv head
+    int parts;              // parts of all sequences together, at most
     float scale;
     const int64_t* mask;
     uint16_t* out;
     float* lse;
-    float* part;            // [seqs][kv_heads][splits][max_new * group][D + 2]
+    // where sequences are cut: how many parts of (sequence, row group, head) are done, and the parts' sums
+    uint32_t* done;         // [seqs][row_groups][kv_heads], 0 before and after the call
+    float* sums;            // [parts][row_groups][kv_heads][part_floats]
 };
 
-// How sequence b is cut: tokens, tokens a part.
-struct Cut {
-    int len, chunk;
-};
-__device__ __forceinline__ Cut cut_of(const AttendParams& a, const NewTokens& t) {
-    const int64_t cap = a.s.width << a.s.page_shift;
-    const int64_t end = static_cast<int64_t>(t.pos0) + t.n;
-    Cut c;
-    c.len = static_cast<int>(end < cap ? end : cap);
-    int chunk = a.chunk;
-    if (c.len > static_cast<int64_t>(chunk) * a.splits) {
-        const int each = (c.len + a.splits - 1) / a.splits;
-        chunk = (each + 31) / 32 * 32;
-    }
-    c.chunk = chunk;
-    return c;
-}
+// Floats of one part's sums: rows of D values, then (R, l) of each row.
+constexpr int part_floats(int dim, int row_tiles) { return 16 * row_tiles * (dim + 2); }
 
 namespace {
 
@@ -128,17 +124,13 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
         static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) char*)p)));
 }
 
-// Two fp32 values -> fp16 halves.  Nearest for fp16 outputs; toward zero (one
-// instruction) for bf16 ones, whose 8 bits do not see the 11th.
-template <int DT>
+// Two fp32 values -> fp16 halves, to nearest.  (Toward zero would be biased:
+// over 131071 tokens the code part of the sum then no longer cancels the bias
+// part, 1.3 % of the result off.)
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    if constexpr (DT == DT_F16) {
-        const uint32_t a = __builtin_bit_cast(uint16_t, static_cast<_Float16>(lo));
-        const uint32_t b = __builtin_bit_cast(uint16_t, static_cast<_Float16>(hi));
-        return a | (b << 16);
-    } else {
-        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(lo, hi));
-    }
+    typedef float float2_t __attribute__((ext_vector_type(2)));
+    typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((float2_t{lo, hi}), half2_t));
 }
 
 // A word of 8 codes -> codes (0, 4), 16 x (1, 5), (2, 6), 16 x (3, 7), times 2^-24.
@@ -164,6 +156,117 @@ __device__ __forceinline__ void load_words(const uint32_t* p, uint32_t (&w)[N]) 
             w[4 * i] = a.x; w[4 * i + 1] = a.y; w[4 * i + 2] = a.z; w[4 * i + 3] = a.w;
         }
     }
+}
+
+// Two floats to and from memory that other XCDs' workgroups read and write in the same launch.
+__device__ __forceinline__ void store_shared(float* p, float x, float y) {
+    const uint64_t v = __builtin_bit_cast(uint32_t, x) | (static_cast<uint64_t>(__builtin_bit_cast(uint32_t, y)) << 32);
+    __hip_atomic_store(reinterpret_cast<uint64_t*>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 load_shared(const float* p) {
+    const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return make_float2(__builtin_bit_cast(float, static_cast<uint32_t>(v)),
+                       __builtin_bit_cast(float, static_cast<uint32_t>(v >> 32)));
+}
+
+// Sum over the wavefront, in every lane.
+__device__ __forceinline__ int wave_sum(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x128, 0xf, 0xf, true);  // rotations within 16 lanes: by 8, 4, 2, 1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x124, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x122, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x121, 0xf, 0xf, true);
+    uint32_t a = v, b = v;
+    swap16(a, b);
+    a = b = a + b;
+    swap32(a, b);
+    return static_cast<int>(a + b);
+}
+
+// Which part of which sequence the unit-th workgroup (of a head and row
+// group) takes: chunks [first, first + chunks) of sequence b, part `part` of
+// `parts`; b < 0: none.
+struct Part {
+    int b, part, parts, first, chunks, slot0;  // slot0: number of the sequence's first part
+};
+
+// Every sequence gets ceil(chunks / T) parts with the least T (up to where
+// the search stops) for which they are at most `parts` together: all
+// workgroups then take about T chunks whatever the lengths are.  Each
+// workgroup finds the cut by itself from the lengths, 64 a register.
+__device__ __forceinline__ Part find_part(const Seqs& s, int unit, int parts, int lane) {
+    Part p;
+    p.part = 0;
+    p.parts = 1;
+    p.first = 0;
+    p.slot0 = unit;
+    p.b = unit < s.seqs ? unit : -1;
+    p.chunks = INT32_MAX / kChunk;
+    if (parts <= s.seqs) return p;  // one part each
+    const int64_t cap = s.width << s.page_shift;
+    int c[kPlanLanes], total = 0;
+#pragma unroll
+    for (int k = 0; k < kPlanLanes; ++k) {
+        const int b = 64 * k + lane;
+        c[k] = 0;
+        if (64 * k < s.seqs && b < s.seqs) {
+            const int64_t len = s.lens[b];
+            c[k] = static_cast<int>(((len < cap ? len : cap) + kChunk - 1) / kChunk);
+            c[k] = c[k] > 0 ? c[k] : 1;
+        }
+        total += c[k];
+    }
+    total = wave_sum(total);
+    // (divisions by T through its fp32 reciprocal: all workgroups do the same, which is all that counts)
+    auto parts_at = [&](int k, float inv) {
+        return c[k] == 0 ? 0 : static_cast<int>((static_cast<float>(c[k]) - 0.5f) * inv) + 1;
+    };
+    auto fits = [&](int t) {
+        const float inv = 1.0f / static_cast<float>(t);
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < kPlanLanes; ++k) n += parts_at(k, inv);
+        return __builtin_amdgcn_readfirstlane(wave_sum(n)) <= parts;
+    };
+    const uint32_t sum = __builtin_amdgcn_readfirstlane(total);
+    // sum / parts <= T, and with T = sum / (parts - seqs) there surely are enough
+    int lo = static_cast<int>((sum + parts - 1) / static_cast<uint32_t>(parts));
+    int hi = static_cast<int>(sum / static_cast<uint32_t>(parts - s.seqs)) + 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (fits(mid)) hi = mid; else lo = mid + 1;
+    }
+    const float inv = 1.0f / static_cast<float>(lo);
+    // the sequence whose parts hold number `unit`
+    int before = 0;
+    p.b = -1;
+#pragma unroll
+    for (int k = 0; k < kPlanLanes; ++k) {
+        if (64 * k >= s.seqs) break;
+        const int mine = parts_at(k, inv);
+        int upto = mine;  // parts of this lane's sequence and those before it
+#pragma unroll
+        for (int m = 1; m < 64; m *= 2) {
+            const int y = __shfl_up(upto, m);
+            upto += lane >= m ? y : 0;
+        }
+        const uint64_t past = __ballot(before + upto <= unit);  // sequences all of whose parts come before
+        if (past != ~uint64_t{0}) {
+            const int l = __builtin_ctzll(~past);
+            const int n = __builtin_amdgcn_readlane(mine, l);
+            if (64 * k + l < s.seqs && n > 0) {
+                p.b = 64 * k + l;
+                p.parts = n;
+                p.slot0 = before + __builtin_amdgcn_readlane(upto, l) - n;
+                p.part = unit - p.slot0;
+                const uint32_t chunks = __builtin_amdgcn_readlane(c[k], l);
+                p.chunks = static_cast<int>((chunks + n - 1) / static_cast<uint32_t>(n));
+                p.first = p.part * p.chunks;
+            }
+            break;
+        }
+        before += __builtin_amdgcn_readlane(upto, 63);
+    }
+    return p;
 }
 
 // One step is 32 tokens, a run in each part of a record.  A wavefront brings
@@ -209,18 +312,35 @@ template <int D, int GS>
 struct RowTile {
     static constexpr int S = D / 32, G = D / GS, NT = D / 16;
     Frag q[S];        // Q^T operand
-    float qs[G];      // sum of the group's q, times 2^-24
+    Frag qs;          // sums of the groups' q, times 2^-24, in three pieces: slot 8 j + g, piece j
     float cs;         // score -> log2 units
     float m, l;       // M; this lane's share of the sum of p
-    float bias[G];    // this lane's share of sum p (b + 8 s)
+    float4_t zb;      // sums p b (rows 0..7: group) and p s (rows 8..15)
     float4_t z[G];    // sum P'
     float4_t o[NT];
     uint64_t bits;    // new tokens that the row sees
 };
 
+// One value as DT's bits, nearest.
+template <int DT>
+__device__ __forceinline__ uint32_t bits_of(float f) {
+    return DtOps<DT>::rne(f);
+}
+// Two values as DT's halves, nearest.
+template <int DT>
+__device__ __forceinline__ uint32_t pack_dt(float lo, float hi) {
+    typedef float float2_t __attribute__((ext_vector_type(2)));
+    if constexpr (DT == DT_F16) {
+        return pack_f16(lo, hi);
+    } else {
+        typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector((float2_t{lo, hi}), bf16x2_t));
+    }
+}
+
 // Loads row tile's Q: values of row i, d = 32 s + 8 j + e.
 template <int DT, int D, int GS>
-__device__ __forceinline__ void load_q(RowTile<D, GS>& t, const uint16_t* q, bool have, float scale) {
+__device__ __forceinline__ void load_q(RowTile<D, GS>& t, const uint16_t* q, bool have, float scale, int j) {
     constexpr int S = D / 32, G = D / GS;
     float f[S][8];
     float top = 0.0f;
@@ -235,101 +355,110 @@ __device__ __forceinline__ void load_q(RowTile<D, GS>& t, const uint16_t* q, boo
         }
     }
     top = max_j(top);
-    // 2^k: the row's largest value comes to [2^9, 2^10); its smallest that
-    // still counts, 2^-24 of that, is then a normal number also after q / 16
-    int k = top > 0.0f ? 9 - __builtin_amdgcn_frexp_expf(top) + 1 : 0;
+    // 2^k: the row's largest value comes to [2^14, 2^15)
+    int k = top > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
     k = k < -90 ? -90 : k > 120 ? 120 : k;
     const float up = __builtin_ldexpf(scale < 0.0f ? -1.0f : 1.0f, k);
+    float sums[G];
 #pragma unroll
-    for (int g = 0; g < G; ++g) t.qs[g] = 0.0f;
+    for (int g = 0; g < G; ++g) sums[g] = 0.0f;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             f[s][e] *= up;
-            t.qs[32 * s / GS] += f[s][e];
+            sums[32 * s / GS] += f[s][e];
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float m = (e & 1) ? 0.0625f : 1.0f;
-            t.q[s].v[e] = pack_f16<DT_F16>(f[s][e] * m, f[s][e + 4] * m);
+            t.q[s].v[e] = pack_f16(f[s][e] * m, f[s][e + 4] * m);
         }
     }
+    t.qs.v[0] = t.qs.v[1] = t.qs.v[2] = t.qs.v[3] = 0;
 #pragma unroll
-    for (int g = 0; g < G; ++g) t.qs[g] = sum_j(t.qs[g]) * 0x1p-24f;
+    for (int g = 0; g < G; ++g) {
+        const float x = sum_j(sums[g]) * 0x1p-24f;
+        // three pieces of 11 or 8 bits, exact up to 2^-24 of x (fp16: 2^-25, 2^-46 of the row's largest q)
+        const uint32_t h0 = bits_of<DT>(x);
+        const float r1 = x - DtOps<DT>::to_f32(static_cast<uint16_t>(h0));
+        const uint32_t h1 = bits_of<DT>(r1);
+        const uint32_t h2 = bits_of<DT>(r1 - DtOps<DT>::to_f32(static_cast<uint16_t>(h1)));
+        const uint32_t h = j == 0 ? h0 : j == 1 ? h1 : j == 2 ? h2 : 0u;
+        t.qs.v[g / 2] |= h << (16 * (g & 1));
+    }
     // log2(e) * |scale| * 2^24 / 2^k
     t.cs = __builtin_ldexpf(fabsf(scale) * 1.44269504088896f, 24 - k);
 }
 
+// Zero the halves of token pairs (0, 1) and (2, 3) of a bundle that has n tokens.
+__device__ __forceinline__ void keep_tokens(uint32_t& w01, uint32_t& w23, int n) {
+    w01 &= n >= 2 ? ~0u : n == 1 ? 0xFFFFu : 0u;
+    w23 &= n >= 4 ? ~0u : n == 3 ? 0xFFFFu : 0u;
+}
+
 // One step: 32 tokens against the row tiles.  EDGE: `first` is the place of
 // the step's first token among the new ones (negative: before them), `left`
-// how many tokens of the step there are.
+// how many tokens of the step there are (slots past them may hold anything:
+// their scales and biases of V are taken as 0).
 template <int DT, int D, int GS, int RT, bool EDGE>
 __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[RT], float& ref_e, int lane,
                                      int first, int left) {
     using L = Slot<D, GS>;
     constexpr int S = D / 32, G = D / GS, NT = D / 16, C = D / 64;
-    const int j = lane / 16;
-    uint32_t vs[2][G][4];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int g = 0; g < G; ++g) load_words<4>(x + L::kVs + ((4 * t + j) * G + g) * 4, vs[t][g]);
-    if constexpr (EDGE) {
-        // slots past the end may hold anything: their scales and biases of V become 0
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int n = left - (16 * t + 4 * j);
-            const uint32_t m01 = n >= 2 ? ~0u : n == 1 ? 0xFFFFu : 0u;
-            const uint32_t m23 = n >= 4 ? ~0u : n == 3 ? 0xFFFFu : 0u;
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                vs[t][g][0] &= m01;
-                vs[t][g][1] &= m23;
-                vs[t][g][2] &= m01;
-                vs[t][g][3] &= m23;
-            }
-        }
-    }
-    // the largest scale of V among this lane's tokens, against 2^(E + 7)
+    const int i = lane % 16, j = lane / 16;
+    const float4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+
+    // the largest scale of V, against 2^(E + 7): one or two pairs a lane
     float big = 0.0f;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) big = fmaxf(big, half_f32<DT>(vs[t][g][r / 2], r & 1));
+    for (int n = 0; n < (G == 8 ? 2 : 1); ++n) {
+        const int at = (lane + 64 * n) % (16 * G);  // (bundle, group), pair
+        uint32_t w = x[L::kVs + (at >> 1) * 4 + (at & 1)];
+        if constexpr (EDGE) {
+            const int tokens = left - (at >> 1) / G * 4 - 2 * (at & 1);
+            w &= tokens >= 2 ? ~0u : tokens == 1 ? 0xFFFFu : 0u;
+        }
+        big = fmaxf(big, fmaxf(half_f32<DT>(w, 0), half_f32<DT>(w, 1)));
+    }
 
-    // scores of all row tiles: sum_g s (codes . q) + b (sum of q)
+    // scores of all row tiles: sum_g b (sum of q) from the matrix core, + s (codes . q)
     float sc[RT][2][4];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        float4_t p[RT][G];
         uint32_t k[S];
-        load_words<S>(x + t * (L::kCodes / 2) + (4 * (lane % 16) + j) * S, k);
+        load_words<S>(x + t * (L::kCodes / 2) + (4 * i + j) * S, k);
+        Frag kb;
+        kb.v[0] = kb.v[1] = kb.v[2] = kb.v[3] = 0;
+        const uint16_t* hb = reinterpret_cast<const uint16_t*>(x + L::kKs) + ((4 * t + i / 4) * G) * 8 + 4 + i % 4;
+#pragma unroll
+        for (int g = 0; g < G; ++g) kb.v[g / 2] |= static_cast<uint32_t>(hb[8 * g]) << (16 * (g & 1));
+        float4_t acc[RT], p[RT][G];
+#pragma unroll
+        for (int u = 0; u < RT; ++u) acc[u] = mf::mfma<DT>(kb, rows[u].qs, zero);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const Frag a = codes8(k[s]);
+            const int g = 32 * s / GS;
 #pragma unroll
             for (int u = 0; u < RT; ++u) {
-                const int g = 32 * s / GS;
-                const float4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
-                p[u][g] = mf::mfma<DT_F16>(a, rows[u].q[s], 32 * s % GS == 0 ? zero : p[u][g]);
+                if (32 * s % GS == 0) p[u][g] = mf::mfma<DT_F16>(a, rows[u].q[s], zero);
+                else p[u][g] = mf::mfma<DT_F16>(a, rows[u].q[s], p[u][g]);
             }
         }
 #pragma unroll
+        for (int u = 0; u < RT; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sc[u][t][r] = acc[u][r];
+#pragma unroll
         for (int g = 0; g < G; ++g) {
-            uint32_t w[4];
-            load_words<4>(x + L::kKs + ((4 * t + j) * G + g) * 4, w);
+            uint32_t w[2];
+            load_words<2>(x + L::kKs + ((4 * t + j) * G + g) * 4, w);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const float ks = half_f32<DT>(w[r / 2], r & 1);
-                const float kb = half_f32<DT>(w[2 + r / 2], r & 1);
 #pragma unroll
-                for (int u = 0; u < RT; ++u) {
-                    const float before = g == 0 ? kb * rows[u].qs[0] : __builtin_fmaf(kb, rows[u].qs[g], sc[u][t][r]);
-                    sc[u][t][r] = __builtin_fmaf(ks, p[u][g][r], before);
-                }
+                for (int u = 0; u < RT; ++u) sc[u][t][r] = __builtin_fmaf(ks, p[u][g][r], sc[u][t][r]);
             }
         }
     }
@@ -355,8 +484,15 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
     }
     if (__any(move)) {
         const float old_e = ref_e;
-        const float all = max_j(big);
-        if (all > 0.0f) ref_e = fmaxf(ref_e, fminf(static_cast<float>(__builtin_amdgcn_frexp_expf(all)), 100.0f));
+        float all = big;
+#pragma unroll
+        for (int n = 1; n < 16; n *= 2) all = fmaxf(all, __shfl_xor(all, n));
+        all = max_j(all);
+        if (all > 0.0f) {
+            // fp16: p itself, up to 2^(8 - E), is an operand as well
+            constexpr float lowest = DT == DT_F16 ? -6.0f : -100.0f;
+            ref_e = fmaxf(ref_e, fminf(fmaxf(static_cast<float>(__builtin_amdgcn_frexp_expf(all)), lowest), 100.0f));
+        }
 #pragma unroll
         for (int u = 0; u < RT; ++u) {
             const float m = fmaxf(rows[u].m, max_j(top[u]));
@@ -364,65 +500,87 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
             rows[u].m = m;
             rows[u].l *= f;
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                rows[u].bias[g] *= f;
+            for (int r = 0; r < 4; ++r) rows[u].zb[r] *= f;
+#pragma unroll
+            for (int g = 0; g < G; ++g)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) rows[u].z[g][r] *= f;
-            }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) rows[u].o[n][r] *= f;
         }
     }
-    // p, its sum, P' and the bias sums
-    Frag pp[RT][G];
+    // p, its sum, and p as an operand
+    Frag p16[RT];
 #pragma unroll
     for (int u = 0; u < RT; ++u) {
         const float ref = rows[u].m + ref_e;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            float p[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                p[r] = exp2_fast(__builtin_fmaf(sc[u][t][r], rows[u].cs, -ref));
-                if constexpr (EDGE) p[r] = see[u][t][r] ? p[r] : 0.0f;
-                rows[u].l += p[r];
+                float p = exp2_fast(__builtin_fmaf(sc[u][t][r], rows[u].cs, -ref));
+                if constexpr (EDGE) p = see[u][t][r] ? p : 0.0f;
+                sc[u][t][r] = p;
+                rows[u].l += p;
             }
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                float s[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    s[r] = half_f32<DT>(vs[t][g][r / 2], r & 1);
-                    const float mid = __builtin_fmaf(8.0f, s[r], half_f32<DT>(vs[t][g][2 + r / 2], r & 1));
-                    rows[u].bias[g] = __builtin_fmaf(p[r], mid, rows[u].bias[g]);
-                }
-                pp[u][g].v[2 * t] = pack_f16<DT>(p[0] * s[0], p[1] * s[1]);
-                pp[u][g].v[2 * t + 1] = pack_f16<DT>(p[2] * s[2], p[3] * s[3]);
-            }
+            p16[u].v[2 * t] = pack_dt<DT>(sc[u][t][0], sc[u][t][1]);
+            p16[u].v[2 * t + 1] = pack_dt<DT>(sc[u][t][2], sc[u][t][3]);
         }
-        Frag ones;
-        ones.v[0] = ones.v[1] = ones.v[2] = ones.v[3] = 0x3C003C00u;
-#pragma unroll
-        for (int g = 0; g < G; ++g) rows[u].z[g] = mf::mfma<DT_F16>(ones, pp[u][g], rows[u].z[g]);
     }
-    // the second product: tile n = 4 c + q of 16 d, from nibble q of the words of quad c
+    // sums of p b and p s, raw scales and biases as the operand: row i < 8 is
+    // the bias of group i mod G, row 8 + i its scale.  (p is rounded, but
+    // alike for both, so that the error is weighed by b + 8 s, small.)
+    {
+        Frag sb;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            uint32_t w[2];
+            load_words<2>(x + L::kVs + ((4 * t + j) * G + i % G) * 4 + (i < 8 ? 2 : 0), w);
+            if constexpr (EDGE) keep_tokens(w[0], w[1], left - (16 * t + 4 * j));
+            sb.v[2 * t] = w[0];
+            sb.v[2 * t + 1] = w[1];
+        }
+#pragma unroll
+        for (int u = 0; u < RT; ++u) rows[u].zb = mf::mfma<DT>(sb, p16[u], rows[u].zb);
+    }
+    // P' and the second product: tile n = 4 c + q of 16 d, from nibble q of the words of quad c
+    Frag ones;
+    ones.v[0] = ones.v[1] = ones.v[2] = ones.v[3] = 0x3C003C00u;
     uint32_t v[2][S];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) load_words<S>(x + L::kV + t * (L::kCodes / 2) + 16 * S * j + S * (lane % 16), v[t]);
+    for (int t = 0; t < 2; ++t) load_words<S>(x + L::kV + t * (L::kCodes / 2) + 16 * S * j + S * i, v[t]);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        uint32_t w[4] = {v[0][c], v[0][C + c], v[1][c], v[1][C + c]};
-        uint32_t h[4] = {w[0] >> 8, w[1] >> 8, w[2] >> 8, w[3] >> 8};
+    for (int g = 0; g < G; ++g) {
+        Frag pp[RT];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int t = 0; t < 2; ++t) {
+            uint32_t w[2];
+            load_words<2>(x + L::kVs + ((4 * t + j) * G + g) * 4, w);
+            if constexpr (EDGE) keep_tokens(w[0], w[1], left - (16 * t + 4 * j));
+            float s[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[r] = half_f32<DT>(w[r / 2], r & 1);
+#pragma unroll
+            for (int u = 0; u < RT; ++u) {
+                pp[u].v[2 * t] = pack_f16(sc[u][t][0] * s[0], sc[u][t][1] * s[1]);
+                pp[u].v[2 * t + 1] = pack_f16(sc[u][t][2] * s[2], sc[u][t][3] * s[3]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < RT; ++u) rows[u].z[g] = mf::mfma<DT_F16>(ones, pp[u], rows[u].z[g]);
+#pragma unroll
+        for (int n = g * (GS / 16); n < (g + 1) * (GS / 16); ++n) {
+            const int c = n / 4, q = n % 4;
             Frag a;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) a.v[k] = (q < 2 ? w[k] : h[k]) & ((q & 1) ? 0x00F000F0u : 0x000F000Fu);
-            const int n = 4 * c + q;
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t w = v[k / 2][(k & 1) * C + c];
+                a.v[k] = (q < 2 ? w : w >> 8) & ((q & 1) ? 0x00F000F0u : 0x000F000Fu);
+            }
 #pragma unroll
-            for (int u = 0; u < RT; ++u) rows[u].o[n] = mf::mfma<DT_F16>(a, pp[u][16 * n / GS], rows[u].o[n]);
+            for (int u = 0; u < RT; ++u) rows[u].o[n] = mf::mfma<DT_F16>(a, pp[u], rows[u].o[n]);
         }
     }
 }
@@ -446,42 +604,35 @@ __global__ __launch_bounds__(64 * kAttendWaves, attend_occupancy(D, RT)) void at
     const int lane = threadIdx.x % 64, i = lane % 16, j = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
-    // workgroups that read the same tokens (row groups) have ids 8 apart: one XCD
-    const int64_t id = blockIdx.x;
-    const int64_t unit = id / (8 * a.row_groups) * 8 + id % 8;
-    const int rg = static_cast<int>(id / 8 % a.row_groups);
-    const int head = static_cast<int>(unit % a.s.kv_heads);
-    const int64_t bp = unit / a.s.kv_heads;
-    const int part = static_cast<int>(bp % a.splits);
-    const int64_t b64 = bp / a.splits;
-    if (b64 >= a.s.seqs) return;
-    const int b = static_cast<int>(b64);
+    // heads fastest; workgroups that read the same tokens (row groups, blockIdx.y) are a multiple of 8 apart: one XCD
+    const uint32_t unit = blockIdx.x / static_cast<uint32_t>(a.s.kv_heads);
+    const int head = static_cast<int>(blockIdx.x - unit * a.s.kv_heads), rg = blockIdx.y;
+    const Part part = find_part(a.s, static_cast<int>(unit), a.parts, lane);
+    const int b = part.b;
+    if (b < 0) return;
     const NewTokens nt = new_tokens(a.s, b);
-    const int count = nt.n * a.group;
+    const int count = nt.n * static_cast<int>(a.group);
     if (rg * 16 * RT >= count) return;
-    const Cut cut = cut_of(a, nt);
-    const int t0 = part * cut.chunk;
-    if (t0 >= cut.len && part > 0) return;
-    const int t1 = t0 + cut.chunk < cut.len ? t0 + cut.chunk : cut.len;
-    const bool whole = cut.len <= cut.chunk;
+    const int64_t cap = a.s.width << a.s.page_shift;
+    const int len = static_cast<int>(nt.pos0 + nt.n < cap ? nt.pos0 + nt.n : cap);
+    const int t0 = part.first * kChunk;
+    const int t1 = len - t0 > part.chunks * kChunk ? t0 + part.chunks * kChunk : len;
 
     RowTile<D, GS> rows[RT];
 #pragma unroll
     for (int u = 0; u < RT; ++u) {
         const int row = (rg * RT + u) * 16 + i;
         const bool have = row < count;
-        const int tok = have ? row / a.group : 0;
+        const int tok = have ? static_cast<uint32_t>(row) / a.group : 0;
         const uint16_t* q = a.q + (nt.row0 + tok) * a.q_row +
-                            (static_cast<int64_t>(head) * a.group + (have ? row % a.group : 0)) * a.q_head + 8 * j;
-        load_q<DT, D, GS>(rows[u], q, have, a.scale);
+                            (static_cast<int64_t>(head) * a.group + (have ? row - tok * static_cast<int>(a.group) : 0)) * a.q_head + 8 * j;
+        load_q<DT, D, GS>(rows[u], q, have, a.scale, j);
         rows[u].bits = !have ? 0 : a.mask != nullptr ? static_cast<uint64_t>(a.mask[nt.row0 + tok]) : ~uint64_t{0} >> (63 - tok);
         rows[u].m = kFar;
         rows[u].l = 0.0f;
+        rows[u].zb = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            rows[u].bias[g] = 0.0f;
-            rows[u].z[g] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        }
+        for (int g = 0; g < G; ++g) rows[u].z[g] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int n = 0; n < NT; ++n) rows[u].o[n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
@@ -518,8 +669,8 @@ __global__ __launch_bounds__(64 * kAttendWaves, attend_occupancy(D, RT)) void at
 #pragma unroll
     for (int n = 0; n < kAttendSlots - 1; ++n)
         there |= fetch(t0 + 32 * wave + n * kStride, n) ? 1u << n : 0u;
-    int slot = 0;
-    for (int t = t0 + 32 * wave; t < t1; t += kStride) {
+    int slot = 0, t = t0 + 32 * wave;
+    auto turn = [&](auto edge) {
         // the slot that the step before this one was read from
         const int free_slot = slot == 0 ? kAttendSlots - 1 : slot - 1;
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -532,29 +683,54 @@ __global__ __launch_bounds__(64 * kAttendWaves, attend_occupancy(D, RT)) void at
             if (after == 0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             else if (after == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L::kLoads) : "memory");
             else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * L::kLoads) : "memory");
-            const uint32_t* x = ring + slot * L::kWords;
-            if (t + 32 > nt.pos0)
-                step<DT, D, GS, RT, true>(x, rows, ref_e, lane, t - nt.pos0, t1 - t);
-            else
-                step<DT, D, GS, RT, false>(x, rows, ref_e, lane, 0, 0);
+            step<DT, D, GS, RT, decltype(edge)::value>(ring + slot * L::kWords, rows, ref_e, lane, t - nt.pos0, t1 - t);
         }
         slot = slot == kAttendSlots - 1 ? 0 : slot + 1;
-    }
+        t += kStride;
+    };
+    // tokens that every row sees, then the new ones and the end
+    const int seen = nt.pos0 < t1 ? nt.pos0 : t1;
+    while (t + 32 <= seen) turn(std::false_type{});
+    while (t < t1) turn(std::true_type{});
     __syncthreads();  // the slots become the sums' buffer
 
     // one set of sums: R and l first
+    float bias[RT][G];
 #pragma unroll
     for (int u = 0; u < RT; ++u) {
         rows[u].l = sum_j(rows[u].l);
+        // sum p (b + 8 s) of group g: rows g and 8 + g of zb, in the lanes j = g / 4 and 2 + g / 4
 #pragma unroll
-        for (int g = 0; g < G; ++g) rows[u].bias[g] = sum_j(rows[u].bias[g]);
+        for (int g = 0; g < G; ++g)
+            bias[u][g] = __shfl(rows[u].zb[g % 4], i + 16 * (g / 4)) + 8.0f * __shfl(rows[u].zb[g % 4], i + 16 * (2 + g / 4));
         if (j == 0) {
             stat[wave][u][i][0] = rows[u].l > 0.0f ? rows[u].m + ref_e : kFar;
             stat[wave][u][i][1] = rows[u].l;
         }
     }
     __syncthreads();
-    const int64_t part_row = ((static_cast<int64_t>(b) * a.s.kv_heads + head) * a.splits + part) * a.s.max_new * a.group;
+    const int64_t group_at = (static_cast<int64_t>(b) * gridDim.y + rg) * a.s.kv_heads + head;
+    auto sums_of = [&](int slot) {
+        return a.sums + ((static_cast<int64_t>(slot) * gridDim.y + rg) * a.s.kv_heads + head) * part_floats(D, RT);
+    };
+    const int base_row = rg * 16 * RT;
+    // one row's values, normalized and rounded
+    auto out_at = [&](int row) {
+        const int tok = static_cast<uint32_t>(row) / a.group;
+        return (nt.row0 + tok) * a.heads + static_cast<int64_t>(head) * a.group + row - tok * static_cast<int>(a.group);
+    };
+    auto put = [&](int64_t at, int d, const float* o, float inv) {
+        uint32_t w[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            w[e] = static_cast<uint32_t>(DtOps<DT>::rne(o[2 * e] * inv)) |
+                   (static_cast<uint32_t>(DtOps<DT>::rne(o[2 * e + 1] * inv)) << 16);
+        *reinterpret_cast<uint2*>(a.out + at * D + d) = make_uint2(w[0], w[1]);
+    };
+    auto put_lse = [&](int64_t at, float ref, float l) {
+        if (a.lse != nullptr)
+            a.lse[at] = l > 0.0f ? 0.693147180559945f * (ref + __builtin_amdgcn_logf(l)) : -__builtin_inff();
+    };
 #pragma unroll
     for (int u = 0; u < RT; ++u) {
         float ref = kFar;
@@ -562,7 +738,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, attend_occupancy(D, RT)) void at
         for (int w = 0; w < kAttendWaves; ++w) ref = fmaxf(ref, stat[w][u][i][0]);
         // (a wavefront that saw nothing has l = 0 and sums of 0)
         const float f = rows[u].l > 0.0f ? exp2_fast(rows[u].m + ref_e - ref) : 0.0f;
-        const int out_row = (rg * RT + u) * 16 + threadIdx.x / 16;
+        const int out_row = base_row + 16 * u + threadIdx.x / 16;
 #pragma unroll
         for (int d0 = 0; d0 < D; d0 += DC) {
 #pragma unroll
@@ -572,7 +748,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, attend_occupancy(D, RT)) void at
                 float4_t v;
 #pragma unroll
                 for (int r2 = 0; r2 < 4; ++r2)
-                    v[r2] = f * (__builtin_fmaf(rows[u].o[n][r2], up, rows[u].bias[g]) - 8.0f * rows[u].z[g][r2]);
+                    v[r2] = f * (__builtin_fmaf(rows[u].o[n][r2], up, bias[u][g]) - 8.0f * rows[u].z[g][r2]);
                 *reinterpret_cast<float4_t*>(&buf[wave][i * kRow + 16 * n - d0 + 4 * j]) = v;
             }
             __syncthreads();
@@ -597,75 +773,104 @@ __global__ __launch_bounds__(64 * kAttendWaves, attend_occupancy(D, RT)) void at
             for (int w = 0; w < kAttendWaves; ++w)
                 l += stat[w][u][oi][1] > 0.0f ? stat[w][u][oi][1] * exp2_fast(stat[w][u][oi][0] - big) : 0.0f;
             if (out_row < count) {
-                if (whole) {
-                    const int tok = out_row / a.group;
-                    const int64_t orow = (nt.row0 + tok) * a.heads + static_cast<int64_t>(head) * a.group + out_row % a.group;
-                    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                    uint32_t w[PER / 2];
+                if (part.parts == 1) {
+                    const int64_t at = out_at(out_row);
 #pragma unroll
-                    for (int e = 0; e < PER / 2; ++e)
-                        w[e] = static_cast<uint32_t>(DtOps<DT>::rne(o[2 * e] * inv)) |
-                               (static_cast<uint32_t>(DtOps<DT>::rne(o[2 * e + 1] * inv)) << 16);
-                    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D + d0 + dd);
-#pragma unroll
-                    for (int e = 0; e < PER / 2; e += 2) *reinterpret_cast<uint2*>(dst + e) = make_uint2(w[e], w[e + 1]);
-                    if (a.lse != nullptr && d0 == 0 && threadIdx.x % 16 == 0)
-                        a.lse[orow] = l > 0.0f ? 0.693147180559945f * (big + __builtin_amdgcn_logf(l)) : -__builtin_inff();
+                    for (int e = 0; e < PER; e += 4) put(at, d0 + dd + e, o + e, l > 0.0f ? 1.0f / l : 0.0f);
+                    if (d0 == 0 && threadIdx.x % 16 == 0) put_lse(at, big, l);
                 } else {
-                    float* dst = a.part + (part_row + out_row) * (D + 2);
+                    float* dst = sums_of(part.slot0 + part.part);
 #pragma unroll
-                    for (int e = 0; e < PER; e += 2) *reinterpret_cast<float2*>(dst + 2 + d0 + dd + e) = make_float2(o[e], o[e + 1]);
-                    if (d0 == 0 && threadIdx.x % 16 == 0) *reinterpret_cast<float2*>(dst) = make_float2(l > 0.0f ? big : kFar, l);
+                    for (int e = 0; e < PER; e += 2) store_shared(dst + (16 * u + oi) * D + d0 + dd + e, o[e], o[e + 1]);
+                    if (d0 == 0 && threadIdx.x % 16 == 0)
+                        store_shared(dst + 16 * RT * D + 2 * (16 * u + oi), l > 0.0f ? big : kFar, l);
                 }
             }
             __syncthreads();
         }
     }
-}
+    if (part.parts == 1) return;
 
-// The parts of sequences that were cut, put together: one wavefront a row.
-template <int DT, int D>
-__global__ __launch_bounds__(256) void attend_join_kernel(AttendParams a) {
-    constexpr int PER = D / 64;
-    const int lane = threadIdx.x % 64;
-    const int per_seq = a.s.max_new * a.heads;
-    const int64_t id = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 64;
-    const int64_t b64 = id / per_seq;
-    if (b64 >= a.s.seqs) return;
-    const int b = static_cast<int>(b64);
-    const NewTokens nt = new_tokens(a.s, b);
-    const int at = static_cast<int>(id % per_seq);
-    const int head = at / (a.s.max_new * a.group), row = at % (a.s.max_new * a.group);
-    if (row >= nt.n * a.group) return;
-    const Cut cut = cut_of(a, nt);
-    if (cut.len <= cut.chunk) return;
-    const int parts = (cut.len + cut.chunk - 1) / cut.chunk;
-    const int64_t stride = static_cast<int64_t>(a.s.max_new) * a.group * (D + 2);
-    const float* p = a.part + ((static_cast<int64_t>(b) * a.s.kv_heads + head) * a.splits * a.s.max_new * a.group + row) * (D + 2);
-    float ref = kFar;
-    for (int k = lane; k < parts; k += 64) ref = fmaxf(ref, p[k * stride]);
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) ref = fmaxf(ref, __shfl_xor(ref, m));
-    float l = 0.0f, o[PER];
-#pragma unroll
-    for (int e = 0; e < PER; ++e) o[e] = 0.0f;
-    for (int k = 0; k < parts; ++k) {
-        const float* c = p + k * stride;
-        const float f = c[1] > 0.0f ? exp2_fast(c[0] - ref) : 0.0f;
-        l += f * c[1];
-#pragma unroll
-        for (int e = 0; e < PER; ++e) o[e] += f * c[2 + lane * PER + e];
+    // The workgroup that finds all other parts done puts them together.  The
+    // sums go through the device's point of coherence (the XCDs' L2 caches
+    // are not coherent): stores and loads of device scope, each thread's
+    // stores waited for before the barrier, the count after it.  (Ordinary
+    // stores behind a device fence write back and drop the whole L2 for every
+    // workgroup: 75 us more for 512 of them.)
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    uint32_t* flag = lds;
+    if (threadIdx.x == 0) {
+        const uint32_t n = __hip_atomic_fetch_add(a.done + group_at, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        flag[0] = n;
+        // the last one leaves the counter as it was found
+        if (n == static_cast<uint32_t>(part.parts) - 1)
+            __hip_atomic_store(a.done + group_at, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    const int64_t orow = (nt.row0 + row / a.group) * a.heads + static_cast<int64_t>(head) * a.group + row % a.group;
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    __syncthreads();
+    if (flag[0] != static_cast<uint32_t>(part.parts) - 1) return;
+    const int left = count - base_row, valid = left < 16 * RT ? left : 16 * RT;
+    // four values a thread; where there are few rows, several threads share the parts of four values
+    constexpr int Q4 = D / 4;
+    const int items = valid * Q4;
+    int share = 1;
+    while (2 * share * items <= 64 * kAttendWaves && share < 8) share *= 2;
+    const float* p0 = sums_of(part.slot0);
+    const int64_t stride = static_cast<int64_t>(gridDim.y) * a.s.kv_heads * part_floats(D, RT);
+    for (int it0 = 0; it0 < items; it0 += 64 * kAttendWaves / share) {
+        const int mine = threadIdx.x % share, it = it0 + threadIdx.x / share;
+        const bool on = it < items;
+        const int row = on ? it / Q4 : 0, d = on ? it % Q4 * 4 : 0;
+        float ref = kFar, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        constexpr int kAhead = 16;
+        for (int k0 = mine; k0 < part.parts; k0 += share * kAhead) {
+            float2 s[kAhead], v[kAhead][2];
 #pragma unroll
-    for (int e = 0; e < PER; ++e) a.out[orow * D + lane * PER + e] = DtOps<DT>::rne(o[e] * inv);
-    if (a.lse != nullptr && lane == 0)
-        a.lse[orow] = l > 0.0f ? 0.693147180559945f * (ref + __builtin_amdgcn_logf(l)) : -__builtin_inff();
+            for (int n = 0; n < kAhead; ++n) {
+                const int k = k0 + n * share;
+                const float* c = p0 + (k < part.parts ? k : k0) * stride;
+                s[n] = load_shared(c + 16 * RT * D + 2 * row);
+                v[n][0] = load_shared(c + row * D + d);
+                v[n][1] = load_shared(c + row * D + d + 2);
+            }
+#pragma unroll
+            for (int n = 0; n < kAhead; ++n)
+                if (k0 + n * share >= part.parts) s[n] = make_float2(kFar, 0.0f);
+            float top = ref;
+#pragma unroll
+            for (int n = 0; n < kAhead; ++n) top = fmaxf(top, s[n].x);
+            const float f0 = exp2_fast(ref - top);
+            l *= f0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] *= f0;
+#pragma unroll
+            for (int n = 0; n < kAhead; ++n) {
+                const float f = s[n].y > 0.0f ? exp2_fast(s[n].x - top) : 0.0f;
+                l = __builtin_fmaf(f, s[n].y, l);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = __builtin_fmaf(f, (e & 1) ? v[n][e / 2].y : v[n][e / 2].x, o[e]);
+            }
+            ref = top;
+        }
+        // the threads that share an item are neighbours
+        for (int m = 1; m < share; m *= 2) {
+            const float r2 = __shfl_xor(ref, m), top = fmaxf(ref, r2);
+            const float f = exp2_fast(ref - top), f2 = exp2_fast(r2 - top);
+            l = l * f + __shfl_xor(l, m) * f2;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = o[e] * f + __shfl_xor(o[e], m) * f2;
+            ref = top;
+        }
+        if (on && mine == 0) {
+            const int64_t at = out_at(base_row + row);
+            put(at, d, o, l > 0.0f ? 1.0f / l : 0.0f);
+            if (d == 0) put_lse(at, ref, l);
+        }
+    }
 }
 
 template <int DT, int D, int GS, int RT, bool NT_LOADS>
-hipError_t launch_attend_kernel(const AttendParams& p, int64_t blocks, hipStream_t st) {
+hipError_t launch_attend_kernel(const AttendParams& p, dim3 grid, hipStream_t st) {
     constexpr int kRow = (D < 128 ? D : 128) + 4;
     constexpr int slots = 4 * kAttendWaves * kAttendSlots * Slot<D, GS>::kWords;
     constexpr int sums = 4 * kAttendWaves * (16 * kRow + RT * 16 * 2);
@@ -676,28 +881,20 @@ hipError_t launch_attend_kernel(const AttendParams& p, int64_t blocks, hipStream
             raise_lds_limit(reinterpret_cast<const void*>(&attend_kernel<DT, D, GS, RT, NT_LOADS>), raised);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((attend_kernel<DT, D, GS, RT, NT_LOADS>), dim3(static_cast<unsigned>(blocks)),
-                       dim3(64 * kAttendWaves), bytes, st, p);
+    hipLaunchKernelGGL((attend_kernel<DT, D, GS, RT, NT_LOADS>), grid, dim3(64 * kAttendWaves), bytes, st, p);
     return hipGetLastError();
 }
 
 template <int DT, int D, int GS, int RT>
-hipError_t run_attend(const AttendParams& p, int64_t blocks, hipStream_t st) {
+hipError_t run_attend(const AttendParams& p, dim3 grid, hipStream_t st) {
     // tokens that several workgroups read stay in L2
-    hipError_t e;
-    if constexpr (RT == 1)
-        e = launch_attend_kernel<DT, D, GS, RT, true>(p, blocks, st);
-    else
-        e = p.row_groups == 1 ? launch_attend_kernel<DT, D, GS, RT, true>(p, blocks, st)
-                              : launch_attend_kernel<DT, D, GS, RT, false>(p, blocks, st);
-    if (e != hipSuccess || p.splits == 1) return e;
-    const int64_t rows = static_cast<int64_t>(p.s.seqs) * p.s.max_new * p.heads;
-    hipLaunchKernelGGL((attend_join_kernel<DT, D>), dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, st, p);
-    return hipGetLastError();
+    if constexpr (RT > 1)
+        if (grid.y > 1) return launch_attend_kernel<DT, D, GS, RT, false>(p, grid, st);
+    return launch_attend_kernel<DT, D, GS, RT, true>(p, grid, st);
 }
 
 // One translation unit per type and head size.
-using AttendFn = hipError_t (*)(const AttendParams&, int64_t, hipStream_t);
+using AttendFn = hipError_t (*)(const AttendParams&, dim3, hipStream_t);
 template <int DT, int D>
 AttendFn attend_fn(int gs, int row_tiles);
 

@@ -14,7 +14,7 @@ import math
 
 import torch
 
-from . import (_DT, _lib, _stream, QMM_ERR_UNSUPPORTED, QmmError, _check, _dev, _dt, _expect, _same_device)
+from . import (_DT, _lib, QMM_ERR_UNSUPPORTED, QmmError, _check, _dev, _dt, _expect, _same_device)
 
 _I32 = torch.int32
 
@@ -37,9 +37,10 @@ def record_words(head_dim: int, group_size: int, page_size: int, dtype=torch.flo
 class KVCache:
     """A pool [layers, pages, kv_heads, words] (int32, GPU, contiguous) and its geometry.
 
-    The pool is the caller's tensor (:meth:`empty` makes one); the object
-    holds it and nothing else, so any number of calls on any streams may use
-    it, ordered by the caller as for any tensor.
+    The pool is the caller's tensor (:meth:`empty` makes one).  Besides it the
+    object keeps, for each stream that :meth:`attend` was called on without a
+    workspace, one workspace; so calls on several streams may overlap, ordered
+    by the caller as for any tensor.
 
     A call works on ``seqs`` sequences: ``tables`` [seqs, width] names their
     pages, ``lens`` [seqs] their lengths with the new tokens counted in.  The
@@ -63,6 +64,7 @@ class KVCache:
         self._geometry = _Geometry(_DT[dtype], group_size, head_dim, kv_heads, page_size, layers, pages,
                                    pool.data_ptr())
         self._c = ctypes.byref(self._geometry)
+        self._spaces: dict[int, torch.Tensor] = {}
         if layers < 1 or kv_heads < 1:
             raise QmmError(QMM_ERR_UNSUPPORTED, f"pool {tuple(pool.shape)}")
 
@@ -139,6 +141,33 @@ class KVCache:
         # (a temporary's block goes back to the caching allocator, which hands it out again in stream order)
         return workspace, workspace.numel() * workspace.element_size()
 
+    def _raw(self, stream) -> int:
+        """Address of the stream of a call (torch's own lookup behind current_stream(), without the object)."""
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.device.index)
+        return int(getattr(stream, "cuda_stream", stream))
+
+    def attend_workspace(self, seqs: int, max_new: int, rows: int, heads: int, max_len: int) -> torch.Tensor:
+        """A workspace for :meth:`attend` calls of up to these sizes (one per stream, or per captured graph)."""
+        need = self.attend_workspace_bytes(seqs, max_new, rows, heads, max_len)
+        return torch.zeros((max(need, 16),), dtype=torch.uint8, device=self.device)
+
+    def _kept_space(self, need: int, stream, raw: int):
+        """The workspace kept for the stream, zeroed when made; a captured call gets its own, zeroed in the graph."""
+        kept = self._spaces.get(raw)
+        if kept is not None and kept.numel() >= need and not torch.cuda.is_current_stream_capturing():
+            return kept
+        if stream is None:
+            made = torch.zeros((need,), dtype=torch.uint8, device=self.device)
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(raw, device=self.device)
+            with torch.cuda.stream(stream):
+                made = torch.zeros((need,), dtype=torch.uint8, device=self.device)
+        if not torch.cuda.is_current_stream_capturing():
+            self._spaces[raw] = made
+        return made
+
     # ---- tokens ----
 
     def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor,
@@ -149,7 +178,7 @@ class KVCache:
             raise ValueError(f"v has shape {tuple(v.shape)}, k {tuple(k.shape)}")
         _check(_lib.qmm_kv_append(*self._seqs(layer, rows, tables, lens, starts, max_new),
                                   *self._rows(k, "k", self.kv_heads), *self._rows(v, "v", self.kv_heads),
-                                  _stream(stream)), "qmm_kv_append")
+                                  self._raw(stream)), "qmm_kv_append")
 
     def read(self, layer: int, rows: int, tables: torch.Tensor, lens: torch.Tensor,
              starts: torch.Tensor | None = None, max_new: int | None = None, stream=None):
@@ -157,7 +186,7 @@ class KVCache:
         args = self._seqs(layer, rows, tables, lens, starts, max_new)
         k = self._new((rows, self.kv_heads, self.head_dim), self.dtype, stream)
         v = self._new(k.shape, self.dtype, stream)
-        _check(_lib.qmm_kv_read(*args, k.data_ptr(), v.data_ptr(), _stream(stream)), "qmm_kv_read")
+        _check(_lib.qmm_kv_read(*args, k.data_ptr(), v.data_ptr(), self._raw(stream)), "qmm_kv_read")
         return k, v
 
     def attend_workspace_bytes(self, seqs: int, max_new: int, rows: int, heads: int, max_len: int) -> int:
@@ -178,6 +207,8 @@ class KVCache:
         whose bit j its word has set.  A row that sees nothing gives zeros.
         ``scale`` defaults to 1/sqrt(head_dim).  ``max_len`` bounds the
         lengths for the split of the work (default: what the tables hold).
+        ``workspace``: from :meth:`attend_workspace` (default: one that the
+        cache keeps for the stream).
         ``lse``: True, or an fp32 tensor [rows, heads], for (out, lse).
         """
         ptr, qr, qh = self._rows(q, "q")
@@ -201,12 +232,18 @@ class KVCache:
             _same_device(q, (mask, "mask"))
         if max_len is None:
             max_len = max(1, args[6] * self.page_size)
-        workspace, nbytes = self._space(workspace, self.attend_workspace_bytes(args[2], args[3], rows, heads, max_len),
-                                        stream)
+        raw = self._raw(stream)
+        if workspace is None:
+            need = self.attend_workspace_bytes(args[2], args[3], rows, heads, max_len)
+            workspace = self._kept_space(need, stream, raw) if need else None
+        else:
+            _dev(workspace, "workspace")
+            _same_device(q, (workspace, "workspace"))
+        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         _check(_lib.qmm_kv_attend(*args, ptr, qr, qh, heads, self._scale if scale is None else scale,
                                   None if mask is None else mask.data_ptr(), out.data_ptr(),
                                   None if lse is False else lse.data_ptr(), max_len,
-                                  None if workspace is None else workspace.data_ptr(), nbytes, _stream(stream)),
+                                  None if workspace is None else workspace.data_ptr(), nbytes, raw),
                "qmm_kv_attend")
         return out if lse is False else (out, lse)
 
@@ -231,7 +268,7 @@ class KVCache:
         """Page dst[i] <- page src[i] in every layer (int32 device tensors)."""
         n = src.numel()
         _check(_lib.qmm_kv_copy_pages(self._c, self._ints(src, "src", (n,)), self._ints(dst, "dst", (n,)), n,
-                                      _stream(stream)), "qmm_kv_copy_pages")
+                                      self._raw(stream)), "qmm_kv_copy_pages")
 
     def reserve(self, tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, add: torch.Tensor,
                 ok: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -243,7 +280,7 @@ class KVCache:
             ok = self._new((seqs,), _I32, stream)
         workspace, nbytes = self._space(workspace, self.pages_workspace_bytes(seqs), stream)
         _check(_lib.qmm_kv_reserve(self._c, *book, ap, self._ints(ok, "ok", (seqs,)),
-                                   None if workspace is None else workspace.data_ptr(), nbytes, _stream(stream)),
+                                   None if workspace is None else workspace.data_ptr(), nbytes, self._raw(stream)),
                "qmm_kv_reserve")
         return ok
 
@@ -260,7 +297,7 @@ class KVCache:
         workspace, nbytes = self._space(workspace, self.pages_workspace_bytes(n), stream)
         _check(_lib.qmm_kv_fork(self._c, *book, self._ints(src, "src", (n,)), self._ints(dst, "dst", (n,)), n,
                                 self._ints(ok, "ok", (n,)), None if workspace is None else workspace.data_ptr(),
-                                nbytes, _stream(stream)), "qmm_kv_fork")
+                                nbytes, self._raw(stream)), "qmm_kv_fork")
         return ok
 
     def free(self, tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, which: torch.Tensor,
@@ -268,7 +305,7 @@ class KVCache:
         """Give up every page of the sequences ``which``; their rows become -1 and their lengths 0."""
         n = which.numel()
         _check(_lib.qmm_kv_free(self._c, *self._book(tables, lens, refs), self._ints(which, "which", (n,)), n,
-                                _stream(stream)), "qmm_kv_free")
+                                self._raw(stream)), "qmm_kv_free")
 
     def compact(self, tables: torch.Tensor, refs: torch.Tensor, tables_out: torch.Tensor | None = None,
                 refs_out: torch.Tensor | None = None, live: torch.Tensor | None = None,
@@ -290,5 +327,5 @@ class KVCache:
         workspace, nbytes = self._space(workspace, self.pages_workspace_bytes(0), stream)
         _check(_lib.qmm_kv_compact(self._c, seqs, tp, width, rp, self._ints(tables_out, "tables_out", (seqs, width)),
                                    self._ints(refs_out, "refs_out", (self.pages,)), self._ints(live, "live", (1,)),
-                                   workspace.data_ptr(), nbytes, _stream(stream)), "qmm_kv_compact")
+                                   workspace.data_ptr(), nbytes, self._raw(stream)), "qmm_kv_compact")
         return tables_out, refs_out

@@ -423,15 +423,19 @@ int qmm_kv_read(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_
  * probabilities (times the scale of their value) are rounded to dt for the
  * second product; one rounding to dt at the end.  Deterministic.
  *
- * max_len: no sequence is longer (1..table_width * page_size); it sets how
- * the tokens are split over workgroups.  Longer ones are still attended to
- * in whole, with the last part longer than planned.
+ * max_len: no sequence is longer (1..table_width * page_size); it bounds how
+ * many parts the sequences are cut into.  Longer ones are still attended to
+ * in whole.
  * workspace: device memory of at least qmm_kv_attend_workspace_bytes(...)
  * bytes, 16-byte aligned (may be NULL when that is 0), not aliasing the
- * other arrays; two calls in flight need two.
+ * other arrays.  Its first QMM_KV_ATTEND_ZEROED_BYTES bytes must be zero
+ * before the first call that uses it; every call leaves them zero (calls of
+ * any sizes may follow each other on one workspace).  Two calls in flight
+ * need two.
  * heads < 1, or not a multiple of kv_heads, max_new > 64 ->
  * QMM_ERR_UNSUPPORTED.
  */
+#define QMM_KV_ATTEND_ZEROED_BYTES 4096
 int64_t qmm_kv_attend_workspace_bytes(const qmm_kv_cache* cache, int64_t seqs, int64_t max_new, int64_t rows,
                                       int64_t heads, int64_t max_len);
 int qmm_kv_attend(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_new, int64_t rows,

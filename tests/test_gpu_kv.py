@@ -293,7 +293,7 @@ def test_step_in_a_graph(Q):
     lens = i32([1, 3])  # as the first replay, so that the warm-up call writes no other place
     q, k, v = (torch.zeros(2, h, dim, dtype=torch.float16, device="cuda") for h in (heads, kv_heads, kv_heads))
     out = torch.zeros_like(q)
-    ws = torch.empty(max(16, graph_cache.attend_workspace_bytes(2, 1, 2, heads, 192)), dtype=torch.uint8, device="cuda")
+    ws = graph_cache.attend_workspace(2, 1, 2, heads, 192)
     step = lambda: (graph_cache.append(0, k, v, tables, lens),
                     graph_cache.attend(0, q, tables, lens, out=out, workspace=ws))
     side = torch.cuda.Stream()
