@@ -1,5 +1,4 @@
 // Attention over the paged 4-bit K/V cache: how a call is cut, and its launch.
-#include <cstdlib>
 #include "qmm_kv_attend.hpp"
 
 namespace qmm {
@@ -19,24 +18,24 @@ struct AttendPlan {
     int64_t bytes;
 };
 
-// Parts for kWorkgroups workgroups over the kv heads and row groups; where
-// the sequences are that many, or short, or too many to plan, one part each.
-constexpr int kWorkgroups = 512;
-static_assert(4 * kWorkgroups <= QMM_KV_ATTEND_ZEROED_BYTES, "a counter for every (sequence, row group, head)");
-
+// Row tiles: 16 rows each, 1 or 2 a wavefront (heads of 256: 1, for the registers).
+// Parts for the workgroups that fill the chip over the kv heads and row
+// groups; where the sequences are that many, or short, or too many to plan,
+// one part each.
 AttendPlan plan_of(const qmm_kv_cache& c, int64_t seqs, int64_t max_new, int64_t heads, int64_t max_len) {
     AttendPlan p;
     const int64_t rows = max_new * (heads / c.kv_heads);
-    p.row_tiles = rows <= 16 ? 1 : 2;
+    p.row_tiles = rows <= 16 || c.head_dim == 256 ? 1 : 2;
     p.row_groups = static_cast<int>((rows + 16 * p.row_tiles - 1) / (16 * p.row_tiles));
     const int64_t each = static_cast<int64_t>(c.kv_heads) * p.row_groups;
-    static const int tgt = getenv("KV_TARGET") ? atoi(getenv("KV_TARGET")) : kWorkgroups;
-    int64_t parts = tgt / each;
+    const int workgroups = attend_workgroups(p.row_tiles);
+    int64_t parts = workgroups / each;
     const int64_t most = seqs * ((max_len + kChunk - 1) / kChunk);
     parts = parts < most ? parts : most;
     if (parts <= seqs || seqs > 64 * kPlanLanes) parts = seqs;
     p.parts = static_cast<int>(parts);
-    // (sequences are cut only where seqs * each < kWorkgroups: the counters fit their fixed place)
+    // (sequences are cut only where seqs * each < workgroups: the counters fit their fixed place)
+    static_assert(4 * kDoneStride * attend_workgroups(1) <= QMM_KV_ATTEND_ZEROED_BYTES, "a counter for each");
     p.bytes = parts > seqs ? QMM_KV_ATTEND_ZEROED_BYTES + parts * each * part_floats(c.head_dim, p.row_tiles) * 4 : 0;
     return p;
 }

@@ -50,16 +50,21 @@
 namespace qmm {
 namespace kv {
 
-constexpr int kAttendWaves = 4;
 constexpr int kAttendSlots = 2;   // steps of a wavefront in LDS: one read, the others on their way
 constexpr float kFar = -3.0e38f;
 
-// Wavefronts a SIMD that the registers are to leave room for.
-constexpr int attend_occupancy(int dim, int row_tiles) { return dim == 256 ? 1 : row_tiles == 1 ? 3 : 2; }
+// Wavefronts of a workgroup, and how many a SIMD the registers are to leave
+// room for.  One row tile: workgroups of 4, for shorter parts.  Two: 8, half
+// as many parts to put together.
+constexpr int attend_waves(int row_tiles) { return row_tiles == 2 ? 8 : 4; }
+constexpr int attend_occupancy(int dim, int row_tiles) { return dim == 256 || row_tiles == 2 ? 2 : 3; }
+// Workgroups that a call is cut into at most: 8 wavefronts a CU.
+constexpr int attend_workgroups(int row_tiles) { return 2048 / attend_waves(row_tiles); }
 
 // The tokens of a sequence are cut into parts of whole chunks, one workgroup
 // a part.
-constexpr int kChunk = 32 * kAttendWaves;
+constexpr int kChunk = 128;
+constexpr int kDoneStride = 32;  // counters lie in lines of their own: device-wide atomics on one line queue up
 constexpr int kPlanLanes = 4;  // sequences a lane holds while the cut is planned: up to 256 are cut
 
 struct AttendParams {
@@ -74,12 +79,12 @@ struct AttendParams {
     uint16_t* out;
     float* lse;
     // where sequences are cut: how many parts of (sequence, row group, head) are done, and the parts' sums
-    uint32_t* done;         // [seqs][row_groups][kv_heads], 0 before and after the call
+    uint32_t* done;         // [seqs][row_groups][kv_heads], kDoneStride apart, 0 before and after the call
     float* sums;            // [parts][row_groups][kv_heads][part_floats]
 };
 
-// Floats of one part's sums: rows of D values, then (R, l) of each row.
-constexpr int part_floats(int dim, int row_tiles) { return 16 * row_tiles * (dim + 2); }
+// Floats of one part's sums: rows of D values, then (R, l, -, -) of each row.
+constexpr int part_floats(int dim, int row_tiles) { return 16 * row_tiles * (dim + 4); }
 
 namespace {
 
@@ -158,15 +163,21 @@ __device__ __forceinline__ void load_words(const uint32_t* p, uint32_t (&w)[N]) 
     }
 }
 
-// Two floats to and from memory that other XCDs' workgroups read and write in the same launch.
-__device__ __forceinline__ void store_shared(float* p, float x, float y) {
-    const uint64_t v = __builtin_bit_cast(uint32_t, x) | (static_cast<uint64_t>(__builtin_bit_cast(uint32_t, y)) << 32);
-    __hip_atomic_store(reinterpret_cast<uint64_t*>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// Values to and from memory that other XCDs' workgroups read and write in the
+// same launch: through the device's point of coherence (the XCDs' L2 caches
+// are not coherent with each other), as device-scope atomics go, but 16 bytes
+// at a time.  `at` is a byte offset from the workspace's sums.  (The 8-byte
+// load builtin of this compiler loads 4.)
+constexpr int kDeviceScope = 16;  // the sc1 bit of a buffer instruction
+using Shared = __amdgpu_buffer_rsrc_t;
+__device__ __forceinline__ Shared shared_of(float* p) {
+    return __builtin_amdgcn_make_buffer_rsrc(p, 0, -1, 0x00027000);
 }
-__device__ __forceinline__ float2 load_shared(const float* p) {
-    const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    return make_float2(__builtin_bit_cast(float, static_cast<uint32_t>(v)),
-                       __builtin_bit_cast(float, static_cast<uint32_t>(v >> 32)));
+__device__ __forceinline__ void store_shared(Shared r, uint32_t at, float4_t v) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(mf::u32x4_t, v), r, at, 0, kDeviceScope);
+}
+__device__ __forceinline__ float4_t load_shared(Shared r, uint32_t at) {
+    return __builtin_bit_cast(float4_t, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, kDeviceScope));
 }
 
 // Sum over the wavefront, in every lane.
@@ -585,6 +596,96 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
     }
 }
 
+// Puts the sums of `parts` parts, the first at byte `at0` and `stride` bytes
+// apart, together for `valid` rows.  An item is four values of a row,
+// consecutive threads take consecutive items; where items are fewer than
+// threads, `share` groups of threads take every share-th part and meet in
+// LDS.  A thread has the values of NI items * NP parts in flight.
+template <int D, int RT, int W, int NI, int NP, class Finish>
+__device__ __forceinline__ void join_parts(Shared sums, uint32_t at0, uint32_t stride, int parts, int valid,
+                                           float* lds, Finish finish) {
+    constexpr int Q4 = D / 4, kThreads = 64 * W;
+    const int items = valid * Q4;
+    int share = 1;
+    while (2 * share * items <= kThreads && share < 8) share *= 2;
+    const int per = kThreads / share, mine = threadIdx.x / per;  // (per: a power of two, at least items where share > 1)
+    for (int it0 = threadIdx.x % per; it0 < items; it0 += NI * per) {
+        float ref[NI], l[NI], o[NI][4];
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+            ref[n] = kFar;
+            l[n] = o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
+        }
+        for (int k0 = mine; k0 < parts; k0 += share * NP) {
+            float2 s[NI][NP];
+            float4_t v[NI][NP];
+#pragma unroll
+            for (int n = 0; n < NI; ++n)
+#pragma unroll
+                for (int m = 0; m < NP; ++m) {
+                    // (no branch around a load, which would wait for it: past the end the last one again)
+                    const int it = it0 + n * per < items ? it0 + n * per : items - 1;
+                    const int k = k0 + m * share < parts ? k0 + m * share : parts - 1;
+                    const uint32_t at = at0 + k * stride;
+                    const float4_t rl = load_shared(sums, at + 4 * (16 * RT * D + 4 * (it / Q4)));
+                    s[n][m] = make_float2(rl[0], rl[1]);
+                    v[n][m] = load_shared(sums, at + 16 * it);
+                }
+#pragma unroll
+            for (int n = 0; n < NI; ++n)
+#pragma unroll
+                for (int m = 0; m < NP; ++m)
+                    if (k0 + m * share >= parts) s[n][m] = make_float2(kFar, 0.0f);
+#pragma unroll
+            for (int n = 0; n < NI; ++n) {
+                float top = ref[n];
+#pragma unroll
+                for (int m = 0; m < NP; ++m) top = fmaxf(top, s[n][m].x);
+                const float f0 = exp2_fast(ref[n] - top);
+                l[n] *= f0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][e] *= f0;
+#pragma unroll
+                for (int m = 0; m < NP; ++m) {
+                    const float f = s[n][m].y > 0.0f ? exp2_fast(s[n][m].x - top) : 0.0f;
+                    l[n] = __builtin_fmaf(f, s[n][m].y, l[n]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[n][e] = __builtin_fmaf(f, v[n][m][e], o[n][e]);
+                }
+                ref[n] = top;
+            }
+        }
+        if (share == 1) {
+#pragma unroll
+            for (int n = 0; n < NI; ++n) {
+                const int it = it0 + n * per;
+                if (it < items) finish(it / Q4, it % Q4 * 4, o[n], ref[n], l[n]);
+            }
+        } else {  // one item a thread: items <= per
+            float* p = lds + (mine * per + it0) * 6;
+            p[0] = ref[0];
+            p[1] = l[0];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[2 + e] = o[0][e];
+        }
+    }
+    if (share > 1) {
+        __syncthreads();
+        if (static_cast<int>(threadIdx.x) < items) {
+            float ref = kFar, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int k = 0; k < share; ++k) ref = fmaxf(ref, lds[(k * per + threadIdx.x) * 6]);
+            for (int k = 0; k < share; ++k) {
+                const float* p = lds + (k * per + threadIdx.x) * 6;
+                const float f = exp2_fast(p[0] - ref);
+                l = __builtin_fmaf(f, p[1], l);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = __builtin_fmaf(f, p[2 + e], o[e]);
+            }
+            finish(threadIdx.x / Q4, threadIdx.x % Q4 * 4, o, ref, l);
+        }
+    }
+}
+
 }  // namespace
 
 // One workgroup: one part of one sequence and kv head against RT tiles of 16
@@ -592,7 +693,8 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
 // wavefronts take the part's steps of 32 tokens in turn, each with sums of
 // its own, which are put together through LDS at the end.
 template <int DT, int D, int GS, int RT, bool NT_LOADS>
-__global__ __launch_bounds__(64 * kAttendWaves, attend_occupancy(D, RT)) void attend_kernel(AttendParams a) {
+__global__ __launch_bounds__(64 * attend_waves(RT), attend_occupancy(D, RT)) void attend_kernel(AttendParams a) {
+    constexpr int kAttendWaves = attend_waves(RT);
     using L = Slot<D, GS>;
     constexpr int G = D / GS, NT = D / 16;
     constexpr int DC = D < 128 ? D : 128;      // values a row that go through LDS at a time
@@ -709,11 +811,14 @@ __global__ __launch_bounds__(64 * kAttendWaves, attend_occupancy(D, RT)) void at
         }
     }
     __syncthreads();
-    const int64_t group_at = (static_cast<int64_t>(b) * gridDim.y + rg) * a.s.kv_heads + head;
-    auto sums_of = [&](int slot) {
-        return a.sums + ((static_cast<int64_t>(slot) * gridDim.y + rg) * a.s.kv_heads + head) * part_floats(D, RT);
+    uint32_t* done = a.done + kDoneStride * ((static_cast<int64_t>(b) * gridDim.y + rg) * a.s.kv_heads + head);
+    const Shared sums = shared_of(a.sums);
+    auto sums_at = [&](int slot) -> uint32_t {  // (all parts' sums are some tens of MB)
+        return ((static_cast<uint32_t>(slot) * gridDim.y + rg) * a.s.kv_heads + head) * (4 * part_floats(D, RT));
     };
     const int base_row = rg * 16 * RT;
+    constexpr int PER = DC * 16 / (64 * kAttendWaves) > 4 ? DC * 16 / (64 * kAttendWaves) : 4;
+    const int oi = threadIdx.x / (DC / PER) % 16, dd = threadIdx.x % (DC / PER) * PER;
     // one row's values, normalized and rounded
     auto out_at = [&](int row) {
         const int tok = static_cast<uint32_t>(row) / a.group;
@@ -738,7 +843,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, attend_occupancy(D, RT)) void at
         for (int w = 0; w < kAttendWaves; ++w) ref = fmaxf(ref, stat[w][u][i][0]);
         // (a wavefront that saw nothing has l = 0 and sums of 0)
         const float f = rows[u].l > 0.0f ? exp2_fast(rows[u].m + ref_e - ref) : 0.0f;
-        const int out_row = base_row + 16 * u + threadIdx.x / 16;
+        const int out_row = base_row + 16 * u + oi;
 #pragma unroll
         for (int d0 = 0; d0 < D; d0 += DC) {
 #pragma unroll
@@ -752,9 +857,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, attend_occupancy(D, RT)) void at
                 *reinterpret_cast<float4_t*>(&buf[wave][i * kRow + 16 * n - d0 + 4 * j]) = v;
             }
             __syncthreads();
-            // thread: row threadIdx / 16, DC / 16 values
-            constexpr int PER = DC / 16;
-            const int oi = threadIdx.x / 16, dd = (threadIdx.x % 16) * PER;
+            // a thread takes PER values of a row
             float o[PER];
 #pragma unroll
             for (int e = 0; e < PER; ++e) o[e] = 0.0f;
@@ -772,18 +875,19 @@ __global__ __launch_bounds__(64 * kAttendWaves, attend_occupancy(D, RT)) void at
 #pragma unroll
             for (int w = 0; w < kAttendWaves; ++w)
                 l += stat[w][u][oi][1] > 0.0f ? stat[w][u][oi][1] * exp2_fast(stat[w][u][oi][0] - big) : 0.0f;
-            if (out_row < count) {
+            if (out_row < count && threadIdx.x < 16 * DC / PER) {
                 if (part.parts == 1) {
                     const int64_t at = out_at(out_row);
 #pragma unroll
                     for (int e = 0; e < PER; e += 4) put(at, d0 + dd + e, o + e, l > 0.0f ? 1.0f / l : 0.0f);
-                    if (d0 == 0 && threadIdx.x % 16 == 0) put_lse(at, big, l);
+                    if (d0 == 0 && dd == 0) put_lse(at, big, l);
                 } else {
-                    float* dst = sums_of(part.slot0 + part.part);
+                    const uint32_t at = sums_at(part.slot0 + part.part);
 #pragma unroll
-                    for (int e = 0; e < PER; e += 2) store_shared(dst + (16 * u + oi) * D + d0 + dd + e, o[e], o[e + 1]);
-                    if (d0 == 0 && threadIdx.x % 16 == 0)
-                        store_shared(dst + 16 * RT * D + 2 * (16 * u + oi), l > 0.0f ? big : kFar, l);
+                    for (int e = 0; e < PER; e += 4)
+                        store_shared(sums, at + 4 * ((16 * u + oi) * D + d0 + dd + e), float4_t{o[e], o[e + 1], o[e + 2], o[e + 3]});
+                    if (d0 == 0 && dd == 0)
+                        store_shared(sums, at + 4 * (16 * RT * D + 4 * (16 * u + oi)), float4_t{l > 0.0f ? big : kFar, l, 0.0f, 0.0f});
                 }
             }
             __syncthreads();
@@ -791,86 +895,41 @@ __global__ __launch_bounds__(64 * kAttendWaves, attend_occupancy(D, RT)) void at
     }
     if (part.parts == 1) return;
 
-    // The workgroup that finds all other parts done puts them together.  The
-    // sums go through the device's point of coherence (the XCDs' L2 caches
-    // are not coherent): stores and loads of device scope, each thread's
-    // stores waited for before the barrier, the count after it.  (Ordinary
-    // stores behind a device fence write back and drop the whole L2 for every
+    // The workgroup that finds all other parts done puts them together.  Each
+    // thread's stores are waited for (they are then at the point of
+    // coherence) before the barrier, the count after it.  (Ordinary stores
+    // behind a device fence write back and drop the whole L2 for every
     // workgroup: 75 us more for 512 of them.)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     uint32_t* flag = lds;
     if (threadIdx.x == 0) {
-        const uint32_t n = __hip_atomic_fetch_add(a.done + group_at, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const uint32_t n = __hip_atomic_fetch_add(done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         flag[0] = n;
         // the last one leaves the counter as it was found
         if (n == static_cast<uint32_t>(part.parts) - 1)
-            __hip_atomic_store(a.done + group_at, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
     if (flag[0] != static_cast<uint32_t>(part.parts) - 1) return;
     const int left = count - base_row, valid = left < 16 * RT ? left : 16 * RT;
-    // four values a thread; where there are few rows, several threads share the parts of four values
-    constexpr int Q4 = D / 4;
-    const int items = valid * Q4;
-    int share = 1;
-    while (2 * share * items <= 64 * kAttendWaves && share < 8) share *= 2;
-    const float* p0 = sums_of(part.slot0);
-    const int64_t stride = static_cast<int64_t>(gridDim.y) * a.s.kv_heads * part_floats(D, RT);
-    for (int it0 = 0; it0 < items; it0 += 64 * kAttendWaves / share) {
-        const int mine = threadIdx.x % share, it = it0 + threadIdx.x / share;
-        const bool on = it < items;
-        const int row = on ? it / Q4 : 0, d = on ? it % Q4 * 4 : 0;
-        float ref = kFar, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        constexpr int kAhead = 16;
-        for (int k0 = mine; k0 < part.parts; k0 += share * kAhead) {
-            float2 s[kAhead], v[kAhead][2];
-#pragma unroll
-            for (int n = 0; n < kAhead; ++n) {
-                const int k = k0 + n * share;
-                const float* c = p0 + (k < part.parts ? k : k0) * stride;
-                s[n] = load_shared(c + 16 * RT * D + 2 * row);
-                v[n][0] = load_shared(c + row * D + d);
-                v[n][1] = load_shared(c + row * D + d + 2);
-            }
-#pragma unroll
-            for (int n = 0; n < kAhead; ++n)
-                if (k0 + n * share >= part.parts) s[n] = make_float2(kFar, 0.0f);
-            float top = ref;
-#pragma unroll
-            for (int n = 0; n < kAhead; ++n) top = fmaxf(top, s[n].x);
-            const float f0 = exp2_fast(ref - top);
-            l *= f0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] *= f0;
-#pragma unroll
-            for (int n = 0; n < kAhead; ++n) {
-                const float f = s[n].y > 0.0f ? exp2_fast(s[n].x - top) : 0.0f;
-                l = __builtin_fmaf(f, s[n].y, l);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] = __builtin_fmaf(f, (e & 1) ? v[n][e / 2].y : v[n][e / 2].x, o[e]);
-            }
-            ref = top;
-        }
-        // the threads that share an item are neighbours
-        for (int m = 1; m < share; m *= 2) {
-            const float r2 = __shfl_xor(ref, m), top = fmaxf(ref, r2);
-            const float f = exp2_fast(ref - top), f2 = exp2_fast(r2 - top);
-            l = l * f + __shfl_xor(l, m) * f2;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = o[e] * f + __shfl_xor(o[e], m) * f2;
-            ref = top;
-        }
-        if (on && mine == 0) {
-            const int64_t at = out_at(base_row + row);
-            put(at, d, o, l > 0.0f ? 1.0f / l : 0.0f);
-            if (d == 0) put_lse(at, ref, l);
-        }
-    }
+    const uint32_t at0 = sums_at(part.slot0), stride = 4 * gridDim.y * a.s.kv_heads * part_floats(D, RT);
+    auto finish = [&](int row, int d, const float* o, float ref, float l) {
+        const int64_t at = out_at(base_row + row);
+        put(at, d, o, l > 0.0f ? 1.0f / l : 0.0f);
+        if (d == 0) put_lse(at, ref, l);
+    };
+    // few parts: more items (four values of a row) of a thread in flight
+    float* meet = reinterpret_cast<float*>(lds) + 64;  // beyond the flag
+    constexpr int W = kAttendWaves;
+    if (part.parts <= 2) join_parts<D, RT, W, 4, 2>(sums, at0, stride, part.parts, valid, meet, finish);
+    else if (part.parts <= 4) join_parts<D, RT, W, 3, 4>(sums, at0, stride, part.parts, valid, meet, finish);
+    else join_parts<D, RT, W, 1, 12>(sums, at0, stride, part.parts, valid, meet, finish);
 }
 
 template <int DT, int D, int GS, int RT, bool NT_LOADS>
 hipError_t launch_attend_kernel(const AttendParams& p, dim3 grid, hipStream_t st) {
+    constexpr int kAttendWaves = attend_waves(RT);
     constexpr int kRow = (D < 128 ? D : 128) + 4;
     constexpr int slots = 4 * kAttendWaves * kAttendSlots * Slot<D, GS>::kWords;
     constexpr int sums = 4 * kAttendWaves * (16 * kRow + RT * 16 * 2);
@@ -888,7 +947,7 @@ hipError_t launch_attend_kernel(const AttendParams& p, dim3 grid, hipStream_t st
 template <int DT, int D, int GS, int RT>
 hipError_t run_attend(const AttendParams& p, dim3 grid, hipStream_t st) {
     // tokens that several workgroups read stay in L2
-    if constexpr (RT > 1)
+    if constexpr (RT > 1 || D == 256)
         if (grid.y > 1) return launch_attend_kernel<DT, D, GS, RT, false>(p, grid, st);
     return launch_attend_kernel<DT, D, GS, RT, true>(p, grid, st);
 }
@@ -901,17 +960,18 @@ AttendFn attend_fn(int gs, int row_tiles);
 }  // namespace kv
 }  // namespace qmm
 
-// Instantiates attend_fn<DT, D> (two row tiles at most 16 rows apart share a wavefront).
-#define QMM_KV_ATTEND_UNIT(DTV, DV)                                                       \
-    namespace qmm {                                                                       \
-    namespace kv {                                                                        \
-    template <>                                                                           \
-    AttendFn attend_fn<DTV, DV>(int gs, int row_tiles) {                                  \
-        if (gs == 32) return row_tiles == 1 ? run_attend<DTV, DV, 32, 1> : run_attend<DTV, DV, 32, 2>; \
-        if (gs == 64) return row_tiles == 1 ? run_attend<DTV, DV, 64, 1> : run_attend<DTV, DV, 64, 2>; \
-        if constexpr (DV >= 128)                                                          \
-            if (gs == 128) return row_tiles == 1 ? run_attend<DTV, DV, 128, 1> : run_attend<DTV, DV, 128, 2>; \
-        return nullptr;                                                                   \
-    }                                                                                     \
-    }                                                                                     \
+// Instantiates attend_fn<DT, D> for 1 or (heads up to 128) 2 row tiles.
+#define QMM_KV_ATTEND_GS(DTV, DV, GSV) \
+    if (gs == GSV) return row_tiles == 1 ? run_attend<DTV, DV, GSV, 1> : run_attend<DTV, DV, GSV, DV == 256 ? 1 : 2>
+#define QMM_KV_ATTEND_UNIT(DTV, DV)                                         \
+    namespace qmm {                                                         \
+    namespace kv {                                                          \
+    template <>                                                             \
+    AttendFn attend_fn<DTV, DV>(int gs, int row_tiles) {                    \
+        QMM_KV_ATTEND_GS(DTV, DV, 32);                                      \
+        QMM_KV_ATTEND_GS(DTV, DV, 64);                                      \
+        if constexpr (DV >= 128) QMM_KV_ATTEND_GS(DTV, DV, 128);            \
+        return nullptr;                                                     \
+    }                                                                       \
+    }                                                                       \
     }

@@ -435,7 +435,7 @@ int qmm_kv_read(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_
  * heads < 1, or not a multiple of kv_heads, max_new > 64 ->
  * QMM_ERR_UNSUPPORTED.
  */
-#define QMM_KV_ATTEND_ZEROED_BYTES 4096
+#define QMM_KV_ATTEND_ZEROED_BYTES 65536
 int64_t qmm_kv_attend_workspace_bytes(const qmm_kv_cache* cache, int64_t seqs, int64_t max_new, int64_t rows,
                                       int64_t heads, int64_t max_len);
 int qmm_kv_attend(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_new, int64_t rows,
