@@ -5,14 +5,14 @@
 //   S[t, row] = sum_g s_K[t, g] (sum_{d in g} q[row, d] c[t, d])  +  b_K[t, g] (sum_{d in g} q[row, d]),
 // so the first product runs on the codes themselves and its result is scaled
 // per token and group; with p = 2^(S - R),
-//   O[row, d] = sum_t (p s_V[t, g]) (c[t, d] - 8)  +  sum_t p (b_V[t, g] + 8 s_V[t, g])
+//   O[row, d] = sum_t (p s_V[t, g]) (c[t, d] - 7.5)  +  sum_t p (b_V[t, g] + 7.5 s_V[t, g])
 // takes the second product's operand P' = p s_V, one per group, to codes
 // again.  Nothing is ever dequantized, and what remains besides the codes --
 // biases of K against sums of q, sums of p b and p s -- are small products
 // of the stored scales and biases as they are, on the matrix cores as well:
 // the vector ALUs bound this kernel.  The codes are centred because P' is
-// rounded to 11 bits: its error is then weighed by |c - 8|, about the size of
-// the values, and not by c; the centring itself is -8 sum_t P', a product
+// rounded to 11 bits: its error is then weighed by |c - 7.5|, about the size of
+// the values, and not by c; the centring itself is -7.5 sum_t P', a product
 // with ones.  R = M + E is a running reference: M follows
 // the scores' maximum and E the exponent of the largest s_V, so that P' stays
 // near 1 whatever the values' size.  Both are moved (and everything summed so
@@ -323,7 +323,7 @@ template <int D, int GS>
 struct RowTile {
     static constexpr int S = D / 32, G = D / GS, NT = D / 16;
     Frag q[S];        // Q^T operand
-    Frag qs;          // sums of the groups' q, times 2^-24, in three pieces: slot 8 j + g, piece j
+    Frag qs;          // sums of the groups' q, times kQsUnit, in three pieces: slot 8 j + g, piece j
     float cs;         // score -> log2 units
     float m, l;       // M; this lane's share of the sum of p
     float4_t zb;      // sums p b (rows 0..7: group) and p s (rows 8..15)
@@ -331,6 +331,12 @@ struct RowTile {
     float4_t o[NT];
     uint64_t bits;    // new tokens that the row sees
 };
+
+// Unit of the sums of q as an operand.  Scores are in units of 2^-24 q; fp16
+// cannot hold the sums' low bits there (2^-25 would be half a unit of a q
+// scaled to 2^15), so they are brought to 2^-9 and their product scaled.
+template <int DT>
+constexpr float kQsUnit = DT == DT_F16 ? 0x1p-9f : 0x1p-24f;
 
 // One value as DT's bits, nearest.
 template <int DT>
@@ -389,8 +395,8 @@ __device__ __forceinline__ void load_q(RowTile<D, GS>& t, const uint16_t* q, boo
     t.qs.v[0] = t.qs.v[1] = t.qs.v[2] = t.qs.v[3] = 0;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-        const float x = sum_j(sums[g]) * 0x1p-24f;
-        // three pieces of 11 or 8 bits, exact up to 2^-24 of x (fp16: 2^-25, 2^-46 of the row's largest q)
+        const float x = sum_j(sums[g]) * kQsUnit<DT>;
+        // three pieces of 11 or 8 bits, exact up to 2^-24 of x (fp16: 2^-25, 2^-31 of the row's largest q)
         const uint32_t h0 = bits_of<DT>(x);
         const float r1 = x - DtOps<DT>::to_f32(static_cast<uint16_t>(h0));
         const uint32_t h1 = bits_of<DT>(r1);
@@ -460,7 +466,7 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
 #pragma unroll
         for (int u = 0; u < RT; ++u)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) sc[u][t][r] = acc[u][r];
+            for (int r = 0; r < 4; ++r) sc[u][t][r] = DT == DT_F16 ? acc[u][r] * (0x1p-24f / kQsUnit<DT>) : acc[u][r];
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             uint32_t w[2];
@@ -542,7 +548,8 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
     }
     // sums of p b and p s, raw scales and biases as the operand: row i < 8 is
     // the bias of group i mod G, row 8 + i its scale.  (p is rounded, but
-    // alike for both, so that the error is weighed by b + 8 s, small.)
+    // alike for both, so that the error is weighed by b + 7.5 s, the middle of the
+    // group's values.)
     {
         Frag sb;
 #pragma unroll
@@ -801,10 +808,10 @@ __global__ __launch_bounds__(64 * attend_waves(RT), attend_occupancy(D, RT)) voi
 #pragma unroll
     for (int u = 0; u < RT; ++u) {
         rows[u].l = sum_j(rows[u].l);
-        // sum p (b + 8 s) of group g: rows g and 8 + g of zb, in the lanes j = g / 4 and 2 + g / 4
+        // sum p (b + 7.5 s) of group g: rows g and 8 + g of zb, in the lanes j = g / 4 and 2 + g / 4
 #pragma unroll
         for (int g = 0; g < G; ++g)
-            bias[u][g] = __shfl(rows[u].zb[g % 4], i + 16 * (g / 4)) + 8.0f * __shfl(rows[u].zb[g % 4], i + 16 * (2 + g / 4));
+            bias[u][g] = __shfl(rows[u].zb[g % 4], i + 16 * (g / 4)) + 7.5f * __shfl(rows[u].zb[g % 4], i + 16 * (2 + g / 4));
         if (j == 0) {
             stat[wave][u][i][0] = rows[u].l > 0.0f ? rows[u].m + ref_e : kFar;
             stat[wave][u][i][1] = rows[u].l;
@@ -853,7 +860,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT), attend_occupancy(D, RT)) voi
                 float4_t v;
 #pragma unroll
                 for (int r2 = 0; r2 < 4; ++r2)
-                    v[r2] = f * (__builtin_fmaf(rows[u].o[n][r2], up, bias[u][g]) - 8.0f * rows[u].z[g][r2]);
+                    v[r2] = f * (__builtin_fmaf(rows[u].o[n][r2], up, bias[u][g]) - 7.5f * rows[u].z[g][r2]);
                 *reinterpret_cast<float4_t*>(&buf[wave][i * kRow + 16 * n - d0 + 4 * j]) = v;
             }
             __syncthreads();

@@ -17,6 +17,7 @@ import torch
 from . import (_DT, _lib, QMM_ERR_UNSUPPORTED, QmmError, _check, _dev, _dt, _expect, _same_device)
 
 _I32 = torch.int32
+ATTEND_ZEROED_BYTES = 65536  # QMM_KV_ATTEND_ZEROED_BYTES
 
 
 class _Geometry(ctypes.Structure):  # qmm_kv_cache
@@ -65,6 +66,7 @@ class KVCache:
                                    pool.data_ptr())
         self._c = ctypes.byref(self._geometry)
         self._spaces: dict[int, torch.Tensor] = {}
+        self._most_space = ATTEND_ZEROED_BYTES + 32768 * (head_dim + 4)  # the bound qmm.h gives
         if layers < 1 or kv_heads < 1:
             raise QmmError(QMM_ERR_UNSUPPORTED, f"pool {tuple(pool.shape)}")
 
@@ -76,14 +78,14 @@ class KVCache:
         pool = torch.empty((layers, pages, kv_heads, words), dtype=_I32, device=device)
         return cls(pool, head_dim, group_size, page_size, dtype)
 
-    # ---- checks ----
+    # ---- checks (a call's host time is a good part of a small step: few attribute reads) ----
 
     def _ints(self, t, name, shape=None):
-        if not isinstance(t, torch.Tensor) or t.dtype is not _I32 or not t.is_contiguous() or t.device != self.device \
-                or (shape is not None and t.shape != shape):
-            raise ValueError(f"{name} must be a contiguous int32 tensor"
-                             f"{'' if shape is None else ' of shape ' + str(tuple(shape))} on {self.device}")
-        return t.data_ptr()
+        if isinstance(t, torch.Tensor) and t.dtype is _I32 and t.is_contiguous() and t.device == self.device \
+                and (shape is None or t.shape == shape):
+            return t.data_ptr()
+        raise ValueError(f"{name} must be a contiguous int32 tensor"
+                         f"{'' if shape is None else ' of shape ' + str(tuple(shape))} on {self.device}")
 
     def _seqs(self, layer, rows, tables, lens, starts, max_new):
         """The arguments from cache to starts that append, read and attend share."""
@@ -92,20 +94,20 @@ class KVCache:
         if tables.dim() != 2:
             raise ValueError(f"tables must be 2-D [seqs, width], got shape {tuple(tables.shape)}")
         seqs, width = tables.shape
-        tp, lp = self._ints(tables, "tables"), self._ints(lens, "lens", (seqs,))
         if starts is None:
             if max_new is None:
                 max_new = rows // seqs if seqs else 0
             if rows != seqs * max_new:
                 raise ValueError(f"{rows} rows are not the same number for each of {seqs} sequences: give starts")
-            sp = None
+            first = None
         else:
             if max_new is None:
                 raise ValueError("starts needs max_new, a bound of one sequence's new tokens")
-            sp = self._ints(starts, "starts", (seqs + 1,))
+            first = self._ints(starts, "starts", (seqs + 1,))
             if rows > seqs * max_new:
                 raise ValueError(f"{rows} rows are more than {seqs} sequences of at most {max_new}")
-        return self._c, layer, seqs, max_new, rows, tp, width, lp, sp
+        return (self._c, layer, seqs, max_new, rows, self._ints(tables, "tables"), width,
+                self._ints(lens, "lens", (seqs,)), first)
 
     def _rows(self, t, name, heads=None):
         """Address and strides of a [rows, heads, head_dim] operand (heads and rows may be strided)."""
@@ -121,20 +123,22 @@ class KVCache:
             raise ValueError(f"{name}'s last axis must be contiguous")
         return t.data_ptr(), r, h
 
-    def _new(self, shape, dtype, stream):
+    def _new(self, shape, strides, dtype, stream):
         """A tensor of this call; where the call runs on another stream than the current one, that stream's."""
         if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return torch.empty_strided(shape, strides, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self._as_stream(stream)):
+            return torch.empty_strided(shape, strides, dtype=dtype, device=self.device)
+
+    def _as_stream(self, stream):
+        return stream if isinstance(stream, torch.cuda.Stream) else \
+            torch.cuda.ExternalStream(int(stream), device=self.device)
 
     def _space(self, workspace, need, stream):
         if workspace is None:
             if need == 0:
                 return None, 0
-            workspace = self._new((need,), torch.uint8, stream)
+            workspace = self._new((need,), (1,), torch.uint8, stream)
         else:
             _dev(workspace, "workspace")
             _same_device(self.pool, (workspace, "workspace"))
@@ -152,21 +156,20 @@ class KVCache:
         need = self.attend_workspace_bytes(seqs, max_new, rows, heads, max_len)
         return torch.zeros((max(need, 16),), dtype=torch.uint8, device=self.device)
 
-    def _kept_space(self, need: int, stream, raw: int):
-        """The workspace kept for the stream, zeroed when made; a captured call gets its own, zeroed in the graph."""
-        kept = self._spaces.get(raw)
-        if kept is not None and kept.numel() >= need and not torch.cuda.is_current_stream_capturing():
-            return kept
-        if stream is None:
-            made = torch.zeros((need,), dtype=torch.uint8, device=self.device)
-        else:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(raw, device=self.device)
-            with torch.cuda.stream(stream):
-                made = torch.zeros((need,), dtype=torch.uint8, device=self.device)
-        if not torch.cuda.is_current_stream_capturing():
-            self._spaces[raw] = made
-        return made
+    def _kept_space(self, stream, raw: int):
+        """The workspace kept for the stream, zeroed when made and large enough for every call; a captured call
+        gets one of its own, zeroed in the graph."""
+        capturing = torch.cuda.is_current_stream_capturing()
+        kept = None if capturing else self._spaces.get(raw)
+        if kept is None:
+            if stream is None:
+                kept = torch.zeros((self._most_space,), dtype=torch.uint8, device=self.device)
+            else:
+                with torch.cuda.stream(self._as_stream(stream)):
+                    kept = torch.zeros((self._most_space,), dtype=torch.uint8, device=self.device)
+            if not capturing:
+                self._spaces[raw] = kept
+        return kept
 
     # ---- tokens ----
 
@@ -184,8 +187,8 @@ class KVCache:
              starts: torch.Tensor | None = None, max_new: int | None = None, stream=None):
         """(k, v) [rows, kv_heads, head_dim]: what ``layer`` holds of the sequences' last tokens, dequantized."""
         args = self._seqs(layer, rows, tables, lens, starts, max_new)
-        k = self._new((rows, self.kv_heads, self.head_dim), self.dtype, stream)
-        v = self._new(k.shape, self.dtype, stream)
+        shape, strides = (rows, self.kv_heads, self.head_dim), (self.kv_heads * self.head_dim, self.head_dim, 1)
+        k, v = self._new(shape, strides, self.dtype, stream), self._new(shape, strides, self.dtype, stream)
         _check(_lib.qmm_kv_read(*args, k.data_ptr(), v.data_ptr(), self._raw(stream)), "qmm_kv_read")
         return k, v
 
@@ -215,13 +218,13 @@ class KVCache:
         rows, heads, _ = q.shape
         args = self._seqs(layer, rows, tables, lens, starts, max_new)
         if out is None:
-            out = self._new((rows, heads, self.head_dim), self.dtype, stream)
+            out = self._new((rows, heads, self.head_dim), (heads * self.head_dim, self.head_dim, 1), self.dtype, stream)
         else:
             _expect(out, "out", (rows, heads, self.head_dim), (self.dtype,))
             _dev(out, "out")
             _same_device(q, (out, "out"))
         if lse is True:
-            lse = self._new((rows, heads), torch.float32, stream)
+            lse = self._new((rows, heads), (heads, 1), torch.float32, stream)
         elif lse is not False:
             _expect(lse, "lse", (rows, heads), (torch.float32,))
             _dev(lse, "lse")
@@ -234,17 +237,15 @@ class KVCache:
             max_len = max(1, args[6] * self.page_size)
         raw = self._raw(stream)
         if workspace is None:
-            need = self.attend_workspace_bytes(args[2], args[3], rows, heads, max_len)
-            workspace = self._kept_space(need, stream, raw) if need else None
+            workspace, nbytes = self._kept_space(stream, raw), self._most_space
         else:
             _dev(workspace, "workspace")
             _same_device(q, (workspace, "workspace"))
-        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+            nbytes = workspace.numel() * workspace.element_size()
         _check(_lib.qmm_kv_attend(*args, ptr, qr, qh, heads, self._scale if scale is None else scale,
                                   None if mask is None else mask.data_ptr(), out.data_ptr(),
                                   None if lse is False else lse.data_ptr(), max_len,
-                                  None if workspace is None else workspace.data_ptr(), nbytes, raw),
-               "qmm_kv_attend")
+                                  workspace.data_ptr(), nbytes, raw), "qmm_kv_attend")
         return out if lse is False else (out, lse)
 
     # ---- pages ----
@@ -277,7 +278,7 @@ class KVCache:
         seqs = book[0]
         ap = self._ints(add, "add", (seqs,))
         if ok is None:
-            ok = self._new((seqs,), _I32, stream)
+            ok = self._new((seqs,), (1,), _I32, stream)
         workspace, nbytes = self._space(workspace, self.pages_workspace_bytes(seqs), stream)
         _check(_lib.qmm_kv_reserve(self._c, *book, ap, self._ints(ok, "ok", (seqs,)),
                                    None if workspace is None else workspace.data_ptr(), nbytes, self._raw(stream)),
@@ -293,7 +294,7 @@ class KVCache:
         book = self._book(tables, lens, refs)
         n = src.numel()
         if ok is None:
-            ok = self._new((n,), _I32, stream)
+            ok = self._new((n,), (1,), _I32, stream)
         workspace, nbytes = self._space(workspace, self.pages_workspace_bytes(n), stream)
         _check(_lib.qmm_kv_fork(self._c, *book, self._ints(src, "src", (n,)), self._ints(dst, "dst", (n,)), n,
                                 self._ints(ok, "ok", (n,)), None if workspace is None else workspace.data_ptr(),
@@ -319,11 +320,11 @@ class KVCache:
         seqs, width = tables.shape
         tp, rp = self._ints(tables, "tables"), self._ints(refs, "refs", (self.pages,))
         if tables_out is None:
-            tables_out = self._new(tables.shape, _I32, stream)
+            tables_out = self._new((seqs, width), (width, 1), _I32, stream)
         if refs_out is None:
-            refs_out = self._new(refs.shape, _I32, stream)
+            refs_out = self._new((self.pages,), (1,), _I32, stream)
         if live is None:
-            live = self._new((1,), _I32, stream)
+            live = self._new((1,), (1,), _I32, stream)
         workspace, nbytes = self._space(workspace, self.pages_workspace_bytes(0), stream)
         _check(_lib.qmm_kv_compact(self._c, seqs, tp, width, rp, self._ints(tables_out, "tables_out", (seqs, width)),
                                    self._ints(refs_out, "refs_out", (self.pages,)), self._ints(live, "live", (1,)),

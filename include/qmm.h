@@ -431,7 +431,8 @@ int qmm_kv_read(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_
  * other arrays.  Its first QMM_KV_ATTEND_ZEROED_BYTES bytes must be zero
  * before the first call that uses it; every call leaves them zero (calls of
  * any sizes may follow each other on one workspace).  Two calls in flight
- * need two.
+ * need two.  No call needs more than QMM_KV_ATTEND_ZEROED_BYTES + 32768 *
+ * (head_dim + 4) bytes.
  * heads < 1, or not a multiple of kv_heads, max_new > 64 ->
  * QMM_ERR_UNSUPPORTED.
  */

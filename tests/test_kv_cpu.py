@@ -95,6 +95,19 @@ def test_attend_workspace_refusals():
     assert L.qmm_kv_attend_workspace_bytes(g, 2, 65, 130, 32, 5) == UNS
 
 
+def test_attend_workspace_bound():
+    """What the header promises no call exceeds, over head layouts, rows, sequences and lengths."""
+    for dim in (64, 128, 256):
+        for kv_heads in (1, 2, 5, 8, 16, 100):
+            for group in (1, 3, 7, 16, 40):
+                for rows in (1, 5, 17, 64):
+                    for seqs in (1, 2, 7, 33, 200, 300):
+                        for most in (1, 129, 5000, 1 << 30):
+                            n = L.qmm_kv_attend_workspace_bytes(geo(dim=dim, kv_heads=kv_heads), seqs, rows, seqs * rows,
+                                                                kv_heads * group, most)
+                            assert 0 <= n <= kv.ATTEND_ZEROED_BYTES + 32768 * (dim + 4)
+
+
 def test_append_and_read_refusals():
     g = geo(pages=9)
     ap = L.qmm_kv_append
