@@ -42,7 +42,7 @@ int check_seqs(const qmm_kv_cache* c, int layer, int64_t seqs, int64_t max_new, 
     if (const int st = check_geometry(c); st != QMM_OK) return st;
     if (layer < 0 || layer >= c->layers || seqs < 0 || max_new < 0 || rows < 0 || width < 0) return QMM_ERR_INVALID_ARG;
     if (seqs > INT32_MAX / 64 || max_new > INT32_MAX / 2 || rows > INT32_MAX ||
-        width > INT32_MAX / c->page_size)
+        width > INT32_MAX / c->page_size || max_new > INT32_MAX / c->kv_heads)
         return QMM_ERR_UNSUPPORTED;
     if (starts == nullptr && rows != seqs * max_new) return QMM_ERR_INVALID_ARG;
     if (starts != nullptr && rows > seqs * max_new) return QMM_ERR_INVALID_ARG;

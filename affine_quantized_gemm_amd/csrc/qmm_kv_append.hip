@@ -7,13 +7,14 @@
 //   q  = s == 0 ? 0 : clamp(rint(fl32(fl32(x - b) / s)), 0, 15);
 // back: RNE_dt(fma(s, q, b)).
 //
-// Appending gives one wavefront a bundle: the four tokens 4u..4u+3 of a page,
-// of one kv head.  That is the unit in which the record keeps V codes
+// Both kernels give one wavefront a bundle: the four tokens 4u..4u+3 of a
+// page, of one kv head.  That is the unit in which the record keeps V codes
 // and scales, so a wavefront writes whole 16-byte runs where all four tokens
 // are new, and no two wavefronts ever write the same 16 bits: a token's codes
 // of V are half-words of their own, and neighbours' slots are left alone.
 // Lane 16 t + c holds token t's values [c D/16, (c + 1) D/16): whole rows are
-// read with 8..32 bytes a lane, and a group is a run of 16 GS / D lanes.
+// read with 8..32 bytes a lane, and a group is a run of 16 GS / D lanes.  The
+// V codes, which the record keeps across rows, change places through LDS.
 #include "qmm_device.hpp"
 #include "qmm_kv.hpp"
 
@@ -23,32 +24,38 @@ namespace {
 
 constexpr int kWaves = 4;
 
-// Unit `id` of the grid: sequence, bundle among those its new tokens touch,
-// kv head.  Heads fastest: neighbouring wavefronts read neighbouring memory.
+// A wavefront's unit: one of the bundles that the new tokens of sequence b
+// touch, and a kv head.  Heads fastest: neighbours read neighbouring memory.
 struct Unit {
     NewTokens t;
-    int head, bundle;  // bundle: position / 4
-    int64_t page;      // -1: nothing here
+    int head, bundle;  // bundle: position / 4, rounded down
+    bool any;          // there are new tokens in it
 };
-__device__ __forceinline__ Unit unit_of(const Seqs& s, int64_t id, int64_t units, int bundles) {
+__device__ __forceinline__ Unit unit_of(const Seqs& s, int b, uint32_t id) {
     Unit u;
-    u.page = -1;
-    if (id >= units) return u;
-    u.head = static_cast<int>(id % s.kv_heads);
-    const int64_t sb = id / s.kv_heads;
-    const int b = static_cast<int>(sb / bundles);
+    const uint32_t at = id / static_cast<uint32_t>(s.kv_heads);
+    u.head = static_cast<int>(id - at * s.kv_heads);
     u.t = new_tokens(s, b);
-    if (u.t.n <= 0) return u;
-    // positions before 0 hold nothing: the first bundle is that of position 0
-    const int first = u.t.pos0 > 0 ? u.t.pos0 : 0;
-    u.bundle = (first >> 2) + static_cast<int>(sb % bundles);
-    if (4 * static_cast<int64_t>(u.bundle) >= static_cast<int64_t>(u.t.pos0) + u.t.n) return u;
-    u.page = page_of(s, b, 4 * u.bundle);
+    u.bundle = (u.t.pos0 >> 2) + static_cast<int>(at);
+    u.any = u.t.n > 0 && 4 * static_cast<int64_t>(u.bundle) < static_cast<int64_t>(u.t.pos0) + u.t.n;
     return u;
 }
 
-// Bundles that n consecutive positions can touch.
-__host__ int bundles_of(int64_t n) { return static_cast<int>((n + 2) / 4 + 1); }
+// Wavefronts a sequence needs: the bundles that n consecutive positions can
+// touch, for every head.
+int64_t units_of(const Seqs& s) { return ((static_cast<int64_t>(s.max_new) + 2) / 4 + 1) * s.kv_heads; }
+
+dim3 grid_of(const Seqs& s) {
+    return dim3(static_cast<unsigned>((units_of(s) + kWaves - 1) / kWaves),
+                static_cast<unsigned>(s.seqs < 65535 ? s.seqs : 65535));
+}
+
+// Place of (token t, value d) in a bundle's codes in LDS, a byte each: the
+// four codes of a half-word side by side.
+template <int D>
+__device__ __forceinline__ int code_at(int t, int d) {
+    return ((t * (D / 64) + d / 64) * 16 + d % 16) * 4 + d % 64 / 16;
+}
 
 template <int N>
 __device__ __forceinline__ void load_values(const uint16_t* p, uint16_t (&v)[N]) {
@@ -84,6 +91,22 @@ __device__ __forceinline__ void store_values(uint16_t* p, const uint16_t (&v)[N]
     }
 }
 
+// Minimum and maximum over runs of LANES lanes (2..16), by exchanges within 16
+// lanes: with the neighbour, the other pair, the other half of 8 (mirrored,
+// its lanes are alike by then), the other 8.
+template <int CTRL>
+__device__ __forceinline__ float from_lane(float v) {
+    const int x = __builtin_bit_cast(int, v);
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(x, x, CTRL, 0xf, 0xf, false));
+}
+template <int LANES>
+__device__ __forceinline__ void group_min_max(float& lo, float& hi) {
+    if constexpr (LANES >= 2) { lo = fminf(lo, from_lane<0xB1>(lo)); hi = fmaxf(hi, from_lane<0xB1>(hi)); }
+    if constexpr (LANES >= 4) { lo = fminf(lo, from_lane<0x4E>(lo)); hi = fmaxf(hi, from_lane<0x4E>(hi)); }
+    if constexpr (LANES >= 8) { lo = fminf(lo, from_lane<0x141>(lo)); hi = fmaxf(hi, from_lane<0x141>(hi)); }
+    if constexpr (LANES >= 16) { lo = fminf(lo, from_lane<0x140>(lo)); hi = fmaxf(hi, from_lane<0x140>(hi)); }
+}
+
 // One operand's N values a lane -> codes; writes the scale and bias of each
 // group (sb: the bundle's first group, 8 half-words a group).
 template <int DT, int D, int GS>
@@ -100,22 +123,34 @@ __device__ __forceinline__ void quantize_lane(const uint16_t (&v)[D / 16], uint3
         lo = fminf(lo, f[i]);
         hi = fmaxf(hi, f[i]);
     }
-#pragma unroll
-    for (int m = 1; m < LANES; m *= 2) {
-        lo = fminf(lo, __shfl_xor(lo, m));
-        hi = fmaxf(hi, __shfl_xor(hi, m));
-    }
+    group_min_max<LANES>(lo, hi);
     lo = __fadd_rn(lo, 0.0f);
     const float s32 = __fdiv_rn(__fsub_rn(hi, lo), 15.0f);
     const uint16_t s_bits = round_up_nonneg<DT>(s32);
     const float s = DtOps<DT>::to_f32(s_bits);
+    // q = rint(fl32((x - lo) / s)), at most 15 as s >= (hi - lo) / 15.  The
+    // division is only carried out where its result could round otherwise
+    // than the product with 1 / s: that is off by less than 2^-21 of at most
+    // 15.1, so within 2^-16 of a half.
+    const float inv = __builtin_amdgcn_rcpf(s);
+    float a[N], t[N];
+    float far = 0.0f;  // largest distance from a whole number
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        q[i] = 0u;
-        if (s != 0.0f) {
-            const float t = __fdiv_rn(__fsub_rn(f[i], lo), s);
-            q[i] = static_cast<uint32_t>(fminf(fmaxf(rintf(t), 0.0f), 15.0f));
-        }
+        a[i] = __fsub_rn(f[i], lo);
+        const float p = a[i] * inv;
+        t[i] = rintf(p);
+        far = fmaxf(far, fabsf(p - t[i]));
+    }
+    // (s = 0, or so small that 1 / s is infinite: the distances are no numbers)
+    if (!(inv < __builtin_inff() && far < 0.5f - 0x1p-16f)) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) t[i] = s != 0.0f ? rintf(__fdiv_rn(a[i], s)) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint32_t x = static_cast<uint32_t>(t[i]);  // (the conversion saturates)
+        q[i] = x < 15u ? x : 15u;
     }
     if (live && c % LANES == 0) {
         uint16_t* p = sb + (c / LANES) * 8 + tok;
@@ -147,152 +182,143 @@ __device__ __forceinline__ void store_k(uint32_t* row, const uint32_t (&q)[D / 1
 }
 
 template <int DT, int D, int GS>
-__global__ __launch_bounds__(64 * kWaves) void append_kernel(Seqs s, int64_t units, int bundles,
-                                                             const uint16_t* __restrict__ k, int64_t k_row,
-                                                             int64_t k_head, const uint16_t* __restrict__ v,
-                                                             int64_t v_row, int64_t v_head) {
+__global__ __launch_bounds__(64 * kWaves) void append_kernel(Seqs s, uint32_t units, const uint16_t* __restrict__ k,
+                                                             int64_t k_row, int64_t k_head,
+                                                             const uint16_t* __restrict__ v, int64_t v_row,
+                                                             int64_t v_head) {
     constexpr int N = D / 16, C = D / 64, G = D / GS;
-    __shared__ uint8_t codes[kWaves][4][D];
+    __shared__ __align__(16) uint8_t codes[kWaves][4 * D];
     const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
     const int tok = lane / 16, c = lane % 16;
     const int page_size = 1 << s.page_shift;
     const Record rec(page_size, D, GS);
-    // every wavefront of the workgroup makes the same number of turns
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * kWaves; base < units;
-         base += static_cast<int64_t>(gridDim.x) * kWaves) {
-        const Unit u = unit_of(s, base + wave, units, bundles);
-        const bool have = u.page >= 0;
-        uint32_t* r = nullptr;
-        int slot = 0, live_bits = 0;
-        uint32_t qv[N];
-        if (have) {
-            r = s.pool + (u.page * s.kv_heads + u.head) * rec.words();
-            slot = (4 * u.bundle) & (page_size - 1);
-            const int i = 4 * u.bundle + tok - u.t.pos0;  // place among the new tokens
-            const bool live = i >= 0 && i < u.t.n;
+    const uint32_t id = blockIdx.x * kWaves + wave;
+    for (int b = blockIdx.y; b < s.seqs; b += gridDim.y) {
+        const Unit u = unit_of(s, b, id);
+        const bool any = id < units && u.any;
+        const int i = 4 * u.bundle + tok - u.t.pos0;  // place among the new tokens
+        const bool live = any && i >= 0 && i < u.t.n;
+        uint16_t kv[N], vv[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) kv[e] = vv[e] = 0;
+        if (live) {
             const int64_t row = u.t.row0 + i;
-            uint16_t kv[N], vv[N];
-#pragma unroll
-            for (int e = 0; e < N; ++e) kv[e] = vv[e] = 0;
-            if (live) {
-                load_values<N>(k + row * k_row + u.head * k_head + c * N, kv);
-                load_values<N>(v + row * v_row + u.head * v_head + c * N, vv);
-            }
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int it = 4 * u.bundle + t - u.t.pos0;
-                live_bits |= (it >= 0 && it < u.t.n) ? 1 << t : 0;
-            }
-            uint32_t qk[N];
+            load_values<N>(k + row * k_row + u.head * k_head + c * N, kv);
+            load_values<N>(v + row * v_row + u.head * v_head + c * N, vv);
+        }
+        const int64_t page = any ? page_of(s, b, 4 * u.bundle) : -1;
+        uint32_t* r = s.pool + (page * s.kv_heads + u.head) * rec.words();  // used where page >= 0
+        const int slot = (4 * u.bundle) & (page_size - 1);
+        if (page >= 0) {
+            uint32_t q[N];
             const int sb = (slot / 4) * G * 4;  // words of the bundles before
-            quantize_lane<DT, D, GS>(kv, qk, reinterpret_cast<uint16_t*>(r + rec.k_sb() + sb), tok, c, live);
-            quantize_lane<DT, D, GS>(vv, qv, reinterpret_cast<uint16_t*>(r + rec.v_sb() + sb), tok, c, live);
-            if (live) store_k<D>(r + rec.k_codes() + (slot + tok) * (D / 8), qk, c);
+            quantize_lane<DT, D, GS>(kv, q, reinterpret_cast<uint16_t*>(r + rec.k_sb() + sb), tok, c, live);
+            if (live) store_k<D>(r + rec.k_codes() + (slot + tok) * (D / 8), q, c);
+            quantize_lane<DT, D, GS>(vv, q, reinterpret_cast<uint16_t*>(r + rec.v_sb() + sb), tok, c, live);
 #pragma unroll
-            for (int e = 0; e < N; ++e) codes[wave][tok][c * N + e] = static_cast<uint8_t>(qv[e]);
+            for (int e = 0; e < N; ++e) codes[wave][code_at<D>(tok, c * N + e)] = static_cast<uint8_t>(q[e]);
         }
         __syncthreads();
-        if (have) {
+        if (page >= 0) {
             // V codes: word (i, p, cc) of the bundle
             uint32_t* dst = r + rec.v_codes() + (slot / 4) * (32 * C);
+            const int first = u.t.pos0 - 4 * u.bundle, last = first + u.t.n;  // new tokens of the bundle: [first, last)
 #pragma unroll
             for (int w0 = 0; w0 < 32 * C; w0 += 64) {
                 const int w = w0 + lane;
                 if (w < 32 * C) {
-                    const int i = w / (2 * C), p = (w / C) % 2, cc = w % C;
+                    const int p = (w / C) % 2, at = code_at<D>(2 * p, 64 * (w % C) + w / (2 * C));
                     uint32_t h[2];
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        h[half] = 0;
-#pragma unroll
-                        for (int n = 0; n < 4; ++n)
-                            h[half] |= static_cast<uint32_t>(codes[wave][2 * p + half][64 * cc + 16 * n + i]) << (4 * n);
+                        // four codes, a byte each, to four nibbles
+                        uint32_t x = *reinterpret_cast<const uint32_t*>(&codes[wave][at + half * D]);
+                        x |= x >> 4;
+                        h[half] = (x & 0xFFu) | ((x >> 8) & 0xFF00u);
                     }
-                    const int both = (live_bits >> (2 * p)) & 3;
-                    if (both == 3) {
-                        dst[w] = h[0] | (h[1] << 16);
-                    } else if (both != 0) {
-                        reinterpret_cast<uint16_t*>(dst + w)[both >> 1] = static_cast<uint16_t>(h[both >> 1]);
-                    }
+                    const bool lo = 2 * p >= first && 2 * p < last, hi = 2 * p + 1 >= first && 2 * p + 1 < last;
+                    if (lo && hi) dst[w] = h[0] | (h[1] << 16);
+                    else if (lo || hi) reinterpret_cast<uint16_t*>(dst + w)[hi ? 1 : 0] = static_cast<uint16_t>(hi ? h[1] : h[0]);
                 }
             }
         }
-        __syncthreads();  // the codes are read before the next turn's are written
+        __syncthreads();  // the codes are read before the next sequence's are written
     }
 }
 
-// Four rows of a sequence and one kv head a wavefront: lane 16 t + c writes
-// values [c D/16, (c + 1) D/16) of row 4 x + t.
 template <int DT, int D, int GS>
-__global__ __launch_bounds__(64 * kWaves) void read_kernel(Seqs s, int64_t units, int quads,
-                                                           uint16_t* __restrict__ k, uint16_t* __restrict__ v) {
-    constexpr int N = D / 16, C = D / 64, G = D / GS, S = D / 32;
+__global__ __launch_bounds__(64 * kWaves) void read_kernel(Seqs s, uint32_t units, uint16_t* __restrict__ k,
+                                                           uint16_t* __restrict__ v) {
+    constexpr int N = D / 16, C = D / 64, G = D / GS, S = D / 32, KW = D / 128 ? D / 128 : 1;
+    __shared__ uint32_t vw[kWaves][32 * C];
     const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-    const int c = lane % 16;
+    const int tok = lane / 16, c = lane % 16;
     const int page_size = 1 << s.page_shift;
     const Record rec(page_size, D, GS);
-    for (int64_t id = static_cast<int64_t>(blockIdx.x) * kWaves + wave; id < units;
-         id += static_cast<int64_t>(gridDim.x) * kWaves) {
-        const int head = static_cast<int>(id % s.kv_heads);
-        const int64_t sq = id / s.kv_heads;
-        const int b = static_cast<int>(sq / quads);
-        const NewTokens t = new_tokens(s, b);
-        const int i = 4 * static_cast<int>(sq % quads) + lane / 16;
-        if (i >= t.n) continue;
-        const int pos = t.pos0 + i;
-        const int64_t page = page_of(s, b, pos);
-        const int slot = pos & (page_size - 1), tok = slot % 4;
-        const uint32_t* r = s.pool + (page * s.kv_heads + head) * rec.words();  // used where page >= 0
-        const int64_t at = ((t.row0 + i) * s.kv_heads + head) * D + c * N;
-        const int sb = ((slot / 4) * G + c * N / GS) * 8 + tok;
+    const uint32_t id = blockIdx.x * kWaves + wave;
+    for (int b = blockIdx.y; b < s.seqs; b += gridDim.y) {
+        const Unit u = unit_of(s, b, id);
+        const bool any = id < units && u.any;
+        const int64_t page = any ? page_of(s, b, 4 * u.bundle) : -1;
+        const uint32_t* r = s.pool + (page * s.kv_heads + u.head) * rec.words();  // used where page >= 0
+        const int slot = (4 * u.bundle) & (page_size - 1);
+        float sc[2] = {0.0f, 0.0f}, bi[2] = {0.0f, 0.0f};
+        uint32_t kw[KW];
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-            uint16_t o[N];
+        for (int x = 0; x < KW; ++x) kw[x] = 0;
+        if (page >= 0) {
+            const int sb = ((slot / 4) * G + c * N / GS) * 8 + tok;
 #pragma unroll
-            for (int e = 0; e < N; ++e) o[e] = 0;
-            if (page >= 0) {
+            for (int part = 0; part < 2; ++part) {
                 const uint16_t* q = reinterpret_cast<const uint16_t*>(r + (part ? rec.v_sb() : rec.k_sb())) + sb;
-                const float sc = DtOps<DT>::to_f32(q[0]), bi = DtOps<DT>::to_f32(q[4]);
+                sc[part] = DtOps<DT>::to_f32(q[0]);
+                bi[part] = DtOps<DT>::to_f32(q[4]);
+            }
+#pragma unroll
+            for (int x = 0; x < KW; ++x) {
+                const int w = c * N / 8 + x;
+                kw[x] = r[rec.k_codes() + (slot + tok) * (D / 8) + (w % 4) * S + w / 4];
+            }
+            const uint32_t* src = r + rec.v_codes() + (slot / 4) * (32 * C);
+#pragma unroll
+            for (int w0 = 0; w0 < 32 * C; w0 += 64)
+                if (w0 + lane < 32 * C) vw[wave][w0 + lane] = src[w0 + lane];
+        }
+        __syncthreads();
+        const int i = 4 * u.bundle + tok - u.t.pos0;
+        if (any && i >= 0 && i < u.t.n) {
+            const int64_t at = ((u.t.row0 + i) * s.kv_heads + u.head) * D + c * N;
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                uint16_t o[N];
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
                     const int d = c * N + e;
-                    uint32_t code;
-                    if (part == 0) {
-                        const int w = d / 8;
-                        code = r[rec.k_codes() + slot * (D / 8) + (w % 4) * S + w / 4] >> (4 * (d % 8));
-                    } else {
-                        const int w = ((d % 16) * 2 + tok / 2) * C + d / 64;
-                        code = r[rec.v_codes() + (slot / 4) * (32 * C) + w] >> (4 * ((d % 64) / 16) + 16 * (tok & 1));
-                    }
-                    o[e] = DtOps<DT>::rne(__fmaf_rn(sc, static_cast<float>(code & 15u), bi));
+                    uint32_t code = 0;
+                    if (part == 0) code = kw[e / 8] >> (D == 64 ? 16 * (c & 1) + 4 * e : 4 * (e % 8));
+                    else if (page >= 0)
+                        code = vw[wave][((d % 16) * 2 + tok / 2) * C + d / 64] >> (4 * ((d % 64) / 16) + 16 * (tok & 1));
+                    o[e] = DtOps<DT>::rne(__fmaf_rn(sc[part], static_cast<float>(code & 15u), bi[part]));
                 }
+                store_values<N>((part ? v : k) + at, o);
             }
-            store_values<N>((part ? v : k) + at, o);
         }
+        __syncthreads();
     }
-}
-
-unsigned grid_of(int64_t units) {
-    const int64_t blocks = (units + kWaves - 1) / kWaves;
-    return static_cast<unsigned>(blocks < (1 << 22) ? blocks : 1 << 22);
 }
 
 template <int DT, int D, int GS>
 hipError_t append_t(const Seqs& s, Rows k, Rows v, hipStream_t st) {
-    const int bundles = bundles_of(s.max_new);
-    const int64_t units = static_cast<int64_t>(s.seqs) * bundles * s.kv_heads;
-    hipLaunchKernelGGL((append_kernel<DT, D, GS>), dim3(grid_of(units)), dim3(64 * kWaves), 0, st, s, units, bundles,
-                       static_cast<const uint16_t*>(k.p), k.stride_row, k.stride_head,
-                       static_cast<const uint16_t*>(v.p), v.stride_row, v.stride_head);
+    hipLaunchKernelGGL((append_kernel<DT, D, GS>), grid_of(s), dim3(64 * kWaves), 0, st, s,
+                       static_cast<uint32_t>(units_of(s)), static_cast<const uint16_t*>(k.p), k.stride_row,
+                       k.stride_head, static_cast<const uint16_t*>(v.p), v.stride_row, v.stride_head);
     return hipGetLastError();
 }
 
 template <int DT, int D, int GS>
 hipError_t read_t(const Seqs& s, void* k, void* v, hipStream_t st) {
-    const int quads = s.max_new / 4 + (s.max_new % 4 != 0);
-    const int64_t units = static_cast<int64_t>(s.seqs) * quads * s.kv_heads;
-    hipLaunchKernelGGL((read_kernel<DT, D, GS>), dim3(grid_of(units)), dim3(64 * kWaves), 0, st, s, units, quads,
-                       static_cast<uint16_t*>(k), static_cast<uint16_t*>(v));
+    hipLaunchKernelGGL((read_kernel<DT, D, GS>), grid_of(s), dim3(64 * kWaves), 0, st, s,
+                       static_cast<uint32_t>(units_of(s)), static_cast<uint16_t*>(k), static_cast<uint16_t*>(v));
     return hipGetLastError();
 }
 
