@@ -22,31 +22,30 @@ namespace qmm {
 namespace kv {
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4;  // the bundles of 16 tokens
 
-// A wavefront's unit: one of the bundles that the new tokens of sequence b
-// touch, and a kv head.  Heads fastest: neighbours read neighbouring memory.
+// A wavefront's unit: a bundle that the new tokens of sequence b touch, and a
+// kv head.  A workgroup has the four bundles of 16 aligned tokens of one head,
+// so that their scales, a line of the record, are written by one XCD.
 struct Unit {
     NewTokens t;
     int head, bundle;  // bundle: position / 4, rounded down
     bool any;          // there are new tokens in it
 };
-__device__ __forceinline__ Unit unit_of(const Seqs& s, int b, uint32_t id) {
+__device__ __forceinline__ Unit unit_of(const Seqs& s, int b, int wave) {
     Unit u;
-    const uint32_t at = id / static_cast<uint32_t>(s.kv_heads);
-    u.head = static_cast<int>(id - at * s.kv_heads);
+    const uint32_t at = blockIdx.x / static_cast<uint32_t>(s.kv_heads);
+    u.head = static_cast<int>(blockIdx.x - at * s.kv_heads);
     u.t = new_tokens(s, b);
-    u.bundle = (u.t.pos0 >> 2) + static_cast<int>(at);
+    u.bundle = ((u.t.pos0 >> 4) + static_cast<int>(at)) * 4 + wave;
     u.any = u.t.n > 0 && 4 * static_cast<int64_t>(u.bundle) < static_cast<int64_t>(u.t.pos0) + u.t.n;
     return u;
 }
 
-// Wavefronts a sequence needs: the bundles that n consecutive positions can
-// touch, for every head.
-int64_t units_of(const Seqs& s) { return ((static_cast<int64_t>(s.max_new) + 2) / 4 + 1) * s.kv_heads; }
-
+// The runs of 16 aligned positions that n consecutive ones can touch, for
+// every head.
 dim3 grid_of(const Seqs& s) {
-    return dim3(static_cast<unsigned>((units_of(s) + kWaves - 1) / kWaves),
+    return dim3(static_cast<unsigned>(((static_cast<int64_t>(s.max_new) + 14) / 16 + 1) * s.kv_heads),
                 static_cast<unsigned>(s.seqs < 65535 ? s.seqs : 65535));
 }
 
@@ -182,7 +181,7 @@ __device__ __forceinline__ void store_k(uint32_t* row, const uint32_t (&q)[D / 1
 }
 
 template <int DT, int D, int GS>
-__global__ __launch_bounds__(64 * kWaves) void append_kernel(Seqs s, uint32_t units, const uint16_t* __restrict__ k,
+__global__ __launch_bounds__(64 * kWaves) void append_kernel(Seqs s, const uint16_t* __restrict__ k,
                                                              int64_t k_row, int64_t k_head,
                                                              const uint16_t* __restrict__ v, int64_t v_row,
                                                              int64_t v_head) {
@@ -192,10 +191,9 @@ __global__ __launch_bounds__(64 * kWaves) void append_kernel(Seqs s, uint32_t un
     const int tok = lane / 16, c = lane % 16;
     const int page_size = 1 << s.page_shift;
     const Record rec(page_size, D, GS);
-    const uint32_t id = blockIdx.x * kWaves + wave;
     for (int b = blockIdx.y; b < s.seqs; b += gridDim.y) {
-        const Unit u = unit_of(s, b, id);
-        const bool any = id < units && u.any;
+        const Unit u = unit_of(s, b, wave);
+        const bool any = u.any;
         const int i = 4 * u.bundle + tok - u.t.pos0;  // place among the new tokens
         const bool live = any && i >= 0 && i < u.t.n;
         uint16_t kv[N], vv[N];
@@ -247,7 +245,7 @@ __global__ __launch_bounds__(64 * kWaves) void append_kernel(Seqs s, uint32_t un
 }
 
 template <int DT, int D, int GS>
-__global__ __launch_bounds__(64 * kWaves) void read_kernel(Seqs s, uint32_t units, uint16_t* __restrict__ k,
+__global__ __launch_bounds__(64 * kWaves) void read_kernel(Seqs s, uint16_t* __restrict__ k,
                                                            uint16_t* __restrict__ v) {
     constexpr int N = D / 16, C = D / 64, G = D / GS, S = D / 32, KW = D / 128 ? D / 128 : 1;
     __shared__ uint32_t vw[kWaves][32 * C];
@@ -255,10 +253,9 @@ __global__ __launch_bounds__(64 * kWaves) void read_kernel(Seqs s, uint32_t unit
     const int tok = lane / 16, c = lane % 16;
     const int page_size = 1 << s.page_shift;
     const Record rec(page_size, D, GS);
-    const uint32_t id = blockIdx.x * kWaves + wave;
     for (int b = blockIdx.y; b < s.seqs; b += gridDim.y) {
-        const Unit u = unit_of(s, b, id);
-        const bool any = id < units && u.any;
+        const Unit u = unit_of(s, b, wave);
+        const bool any = u.any;
         const int64_t page = any ? page_of(s, b, 4 * u.bundle) : -1;
         const uint32_t* r = s.pool + (page * s.kv_heads + u.head) * rec.words();  // used where page >= 0
         const int slot = (4 * u.bundle) & (page_size - 1);
@@ -310,7 +307,7 @@ __global__ __launch_bounds__(64 * kWaves) void read_kernel(Seqs s, uint32_t unit
 template <int DT, int D, int GS>
 hipError_t append_t(const Seqs& s, Rows k, Rows v, hipStream_t st) {
     hipLaunchKernelGGL((append_kernel<DT, D, GS>), grid_of(s), dim3(64 * kWaves), 0, st, s,
-                       static_cast<uint32_t>(units_of(s)), static_cast<const uint16_t*>(k.p), k.stride_row,
+                       static_cast<const uint16_t*>(k.p), k.stride_row,
                        k.stride_head, static_cast<const uint16_t*>(v.p), v.stride_row, v.stride_head);
     return hipGetLastError();
 }
@@ -318,7 +315,7 @@ hipError_t append_t(const Seqs& s, Rows k, Rows v, hipStream_t st) {
 template <int DT, int D, int GS>
 hipError_t read_t(const Seqs& s, void* k, void* v, hipStream_t st) {
     hipLaunchKernelGGL((read_kernel<DT, D, GS>), grid_of(s), dim3(64 * kWaves), 0, st, s,
-                       static_cast<uint32_t>(units_of(s)), static_cast<uint16_t*>(k), static_cast<uint16_t*>(v));
+                       static_cast<uint16_t*>(k), static_cast<uint16_t*>(v));
     return hipGetLastError();
 }
 
