@@ -149,6 +149,19 @@ __device__ __forceinline__ Frag codes8(uint32_t w) {
     return f;
 }
 
+// fp16 halves of two products, each rounded once.
+template <int DT>
+__device__ __forceinline__ uint32_t mul_f16(float p0, float p1, uint32_t w) {
+    if constexpr (DT == DT_F16) {  // one mixed-precision product of the scale as it lies
+        // (half by half: as a vector the compiler converts, multiplies and rounds apart, 40 instructions for 24)
+        const uint32_t a = __builtin_bit_cast(uint16_t, static_cast<_Float16>(p0 * half_f32<DT>(w, 0)));
+        const uint32_t b = __builtin_bit_cast(uint16_t, static_cast<_Float16>(p1 * half_f32<DT>(w, 1)));
+        return a | (b << 16);
+    } else {
+        return pack_f16(p0 * half_f32<DT>(w, 0), p1 * half_f32<DT>(w, 1));
+    }
+}
+
 template <int N>
 __device__ __forceinline__ void load_words(const uint32_t* p, uint32_t (&w)[N]) {
     if constexpr (N == 2) {
@@ -355,19 +368,17 @@ __device__ __forceinline__ uint32_t pack_dt(float lo, float hi) {
     }
 }
 
-// Loads row tile's Q: values of row i, d = 32 s + 8 j + e.
+// Row tile's Q from its words w: values of row i, d = 32 s + 8 j + e.
 template <int DT, int D, int GS>
-__device__ __forceinline__ void load_q(RowTile<D, GS>& t, const uint16_t* q, bool have, float scale, int j) {
+__device__ __forceinline__ void make_q(RowTile<D, GS>& t, const uint32_t (&w)[D / 32][4], float scale, int j) {
     constexpr int S = D / 32, G = D / GS;
     float f[S][8];
     float top = 0.0f;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-        uint32_t w[4] = {0, 0, 0, 0};
-        if (have) load_words<4>(reinterpret_cast<const uint32_t*>(q + 32 * s), w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            f[s][e] = half_f32<DT>(w[e / 2], e & 1);
+            f[s][e] = half_f32<DT>(w[s][e / 2], e & 1);
             top = fmaxf(top, fabsf(f[s][e]));
         }
     }
@@ -375,27 +386,22 @@ __device__ __forceinline__ void load_q(RowTile<D, GS>& t, const uint16_t* q, boo
     // 2^k: the row's largest value comes to [2^14, 2^15)
     int k = top > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
     k = k < -90 ? -90 : k > 120 ? 120 : k;
-    const float up = __builtin_ldexpf(scale < 0.0f ? -1.0f : 1.0f, k);
+    // (odd d meet codes that count 16 times)
+    const float up[2] = {__builtin_ldexpf(scale < 0.0f ? -1.0f : 1.0f, k), __builtin_ldexpf(scale < 0.0f ? -1.0f : 1.0f, k - 4)};
     float sums[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) sums[g] = 0.0f;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            f[s][e] *= up;
-            sums[32 * s / GS] += f[s][e];
-        }
+        for (int e = 0; e < 8; ++e) sums[32 * s / GS] += f[s][e];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float m = (e & 1) ? 0.0625f : 1.0f;
-            t.q[s].v[e] = pack_f16(f[s][e] * m, f[s][e + 4] * m);
-        }
+        for (int e = 0; e < 4; ++e) t.q[s].v[e] = pack_f16(f[s][e] * up[e & 1], f[s][e + 4] * up[e & 1]);
     }
     t.qs.v[0] = t.qs.v[1] = t.qs.v[2] = t.qs.v[3] = 0;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-        const float x = sum_j(sums[g]) * kQsUnit<DT>;
+        const float x = sum_j(sums[g]) * (up[0] * kQsUnit<DT>);
         // three pieces of 11 or 8 bits, exact up to 2^-24 of x (fp16: 2^-25, 2^-31 of the row's largest q)
         const uint32_t h0 = bits_of<DT>(x);
         const float r1 = x - DtOps<DT>::to_f32(static_cast<uint16_t>(h0));
@@ -577,13 +583,10 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
             uint32_t w[2];
             load_words<2>(x + L::kVs + ((4 * t + j) * G + g) * 4, w);
             if constexpr (EDGE) keep_tokens(w[0], w[1], left - (16 * t + 4 * j));
-            float s[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) s[r] = half_f32<DT>(w[r / 2], r & 1);
 #pragma unroll
             for (int u = 0; u < RT; ++u) {
-                pp[u].v[2 * t] = pack_f16(sc[u][t][0] * s[0], sc[u][t][1] * s[1]);
-                pp[u].v[2 * t + 1] = pack_f16(sc[u][t][2] * s[2], sc[u][t][3] * s[3]);
+                pp[u].v[2 * t] = mul_f16<DT>(sc[u][t][0], sc[u][t][1], w[0]);
+                pp[u].v[2 * t + 1] = mul_f16<DT>(sc[u][t][2], sc[u][t][3], w[1]);
             }
         }
 #pragma unroll
@@ -727,7 +730,25 @@ __global__ __launch_bounds__(64 * attend_waves(RT), attend_occupancy(D, RT)) voi
     const int t0 = part.first * kChunk;
     const int t1 = len - t0 > part.chunks * kChunk ? t0 + part.chunks * kChunk : len;
 
-    RowTile<D, GS> rows[RT];
+    const Record rec(1 << a.s.page_shift, D, GS);
+    const int mask_slot = (1 << a.s.page_shift) - 1;
+    // page ids of 64 columns of the table, one a lane
+    int ids, col0;
+    auto load_ids = [&](int col) {
+        col0 = col;
+        const int64_t c = col + lane;
+        ids = c < a.s.width ? a.s.tables[static_cast<int64_t>(b) * a.s.width + c] : -1;
+        if (ids >= a.s.pages) ids = -1;
+    };
+    load_ids(t0 >> a.s.page_shift);
+    auto page_at = [&](int t) -> int {
+        const int col = t >> a.s.page_shift;
+        if (col >= col0 + 64) load_ids(col);
+        return __builtin_amdgcn_readlane(ids, col - col0);
+    };
+    // the rows of q, asked for together with the page ids; worked on while the first tokens come
+    uint32_t qw[RT][D / 32][4];
+    uint64_t bits[RT];
 #pragma unroll
     for (int u = 0; u < RT; ++u) {
         const int row = (rg * RT + u) * 16 + i;
@@ -735,32 +756,19 @@ __global__ __launch_bounds__(64 * attend_waves(RT), attend_occupancy(D, RT)) voi
         const int tok = have ? static_cast<uint32_t>(row) / a.group : 0;
         const uint16_t* q = a.q + (nt.row0 + tok) * a.q_row +
                             (static_cast<int64_t>(head) * a.group + (have ? row - tok * static_cast<int>(a.group) : 0)) * a.q_head + 8 * j;
-        load_q<DT, D, GS>(rows[u], q, have, a.scale, j);
-        rows[u].bits = !have ? 0 : a.mask != nullptr ? static_cast<uint64_t>(a.mask[nt.row0 + tok]) : ~uint64_t{0} >> (63 - tok);
-        rows[u].m = kFar;
-        rows[u].l = 0.0f;
-        rows[u].zb = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int g = 0; g < G; ++g) rows[u].z[g] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s = 0; s < D / 32; ++s) {
+            load_words<4>(reinterpret_cast<const uint32_t*>(q + 32 * s), qw[u][s]);  // (no row: the first one's)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) rows[u].o[n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-    float ref_e = -100.0f;
-
-    const Record rec(1 << a.s.page_shift, D, GS);
-    const int mask_slot = (1 << a.s.page_shift) - 1;
-    // page ids of 64 columns of the table, one a lane
-    int ids = -1, col0 = -64;
-    auto page_at = [&](int t) -> int {
-        const int col = t >> a.s.page_shift;
-        if (col >= col0 + 64) {
-            col0 = col;
-            const int64_t c = col + lane;
-            ids = c < a.s.width ? a.s.tables[static_cast<int64_t>(b) * a.s.width + c] : -1;
-            if (ids >= a.s.pages) ids = -1;
+            for (int e = 0; e < 4; ++e) qw[u][s][e] = have ? qw[u][s][e] : 0;
         }
-        return __builtin_amdgcn_readlane(ids, col - col0);
-    };
+        bits[u] = !have ? 0 : a.mask != nullptr ? static_cast<uint64_t>(a.mask[nt.row0 + tok]) : ~uint64_t{0} >> (63 - tok);
+        // (waited for here: behind the token loads the wait would be for those as well)
+#pragma unroll
+        for (int s = 0; s < D / 32; ++s)
+            asm volatile("" : "+v"(qw[u][s][0]), "+v"(qw[u][s][1]), "+v"(qw[u][s][2]), "+v"(qw[u][s][3]));
+        asm volatile("" : "+v"(bits[u]));
+    }
     uint32_t* ring = lds + wave * (kAttendSlots * L::kWords);
     const uint32_t ring_at = lds_address(ring);
     constexpr int kStride = 32 * kAttendWaves;
@@ -778,6 +786,21 @@ __global__ __launch_bounds__(64 * attend_waves(RT), attend_occupancy(D, RT)) voi
 #pragma unroll
     for (int n = 0; n < kAttendSlots - 1; ++n)
         there |= fetch(t0 + 32 * wave + n * kStride, n) ? 1u << n : 0u;
+    RowTile<D, GS> rows[RT];
+#pragma unroll
+    for (int u = 0; u < RT; ++u) {
+        make_q<DT, D, GS>(rows[u], qw[u], a.scale, j);
+        rows[u].bits = bits[u];
+        rows[u].m = kFar;
+        rows[u].l = 0.0f;
+        rows[u].zb = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int g = 0; g < G; ++g) rows[u].z[g] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) rows[u].o[n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    float ref_e = -100.0f;
+
     int slot = 0, t = t0 + 32 * wave;
     auto turn = [&](auto edge) {
         // the slot that the step before this one was read from
