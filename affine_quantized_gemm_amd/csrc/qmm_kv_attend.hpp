@@ -149,19 +149,6 @@ __device__ __forceinline__ Frag codes8(uint32_t w) {
     return f;
 }
 
-// fp16 halves of two products, each rounded once.
-template <int DT>
-__device__ __forceinline__ uint32_t mul_f16(float p0, float p1, uint32_t w) {
-    if constexpr (DT == DT_F16) {  // one mixed-precision product of the scale as it lies
-        // (half by half: as a vector the compiler converts, multiplies and rounds apart, 40 instructions for 24)
-        const uint32_t a = __builtin_bit_cast(uint16_t, static_cast<_Float16>(p0 * half_f32<DT>(w, 0)));
-        const uint32_t b = __builtin_bit_cast(uint16_t, static_cast<_Float16>(p1 * half_f32<DT>(w, 1)));
-        return a | (b << 16);
-    } else {
-        return pack_f16(p0 * half_f32<DT>(w, 0), p1 * half_f32<DT>(w, 1));
-    }
-}
-
 template <int N>
 __device__ __forceinline__ void load_words(const uint32_t* p, uint32_t (&w)[N]) {
     if constexpr (N == 2) {
@@ -420,13 +407,24 @@ __device__ __forceinline__ void keep_tokens(uint32_t& w01, uint32_t& w23, int n)
     w23 &= n >= 4 ? ~0u : n == 3 ? 0xFFFFu : 0u;
 }
 
+// Issue priority of the wavefront.  The matrix products go first, so that a
+// SIMD's two wavefronts do not do their softmax at the same time; between
+// them the younger wavefront (`late`) goes first, which otherwise falls behind
+// and is left without another to hide its waits.  (64 rows over 16k tokens
+// 118 us, 131 without; verify rows over 8k 39.4, 41.2.)
+__device__ __forceinline__ void priority_products() { __builtin_amdgcn_s_setprio(2); }
+__device__ __forceinline__ void priority_rest(bool late) {
+    if (late) __builtin_amdgcn_s_setprio(1);
+    else __builtin_amdgcn_s_setprio(0);
+}
+
 // One step: 32 tokens against the row tiles.  EDGE: `first` is the place of
 // the step's first token among the new ones (negative: before them), `left`
 // how many tokens of the step there are (slots past them may hold anything:
 // their scales and biases of V are taken as 0).
 template <int DT, int D, int GS, int RT, bool EDGE>
 __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[RT], float& ref_e, int lane,
-                                     int first, int left) {
+                                     int first, int left, bool late) {
     using L = Slot<D, GS>;
     constexpr int S = D / 32, G = D / GS, NT = D / 16, C = D / 64;
     const int i = lane % 16, j = lane / 16;
@@ -445,6 +443,7 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
         big = fmaxf(big, fmaxf(half_f32<DT>(w, 0), half_f32<DT>(w, 1)));
     }
 
+    priority_products();
     // scores of all row tiles: sum_g b (sum of q) from the matrix core, + s (codes . q)
     float sc[RT][2][4];
 #pragma unroll
@@ -485,6 +484,7 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
             }
         }
     }
+    priority_rest(late);
     bool see[RT][2][4];
     float top[RT];
     bool move = big > exp2_fast(ref_e + 7.0f);
@@ -569,6 +569,7 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
 #pragma unroll
         for (int u = 0; u < RT; ++u) rows[u].zb = mf::mfma<DT>(sb, p16[u], rows[u].zb);
     }
+    priority_products();
     // P' and the second product: tile n = 4 c + q of 16 d, from nibble q of the words of quad c
     Frag ones;
     ones.v[0] = ones.v[1] = ones.v[2] = ones.v[3] = 0x3C003C00u;
@@ -583,10 +584,13 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
             uint32_t w[2];
             load_words<2>(x + L::kVs + ((4 * t + j) * G + g) * 4, w);
             if constexpr (EDGE) keep_tokens(w[0], w[1], left - (16 * t + 4 * j));
+            float s[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[r] = half_f32<DT>(w[r / 2], r & 1);
 #pragma unroll
             for (int u = 0; u < RT; ++u) {
-                pp[u].v[2 * t] = mul_f16<DT>(sc[u][t][0], sc[u][t][1], w[0]);
-                pp[u].v[2 * t + 1] = mul_f16<DT>(sc[u][t][2], sc[u][t][3], w[1]);
+                pp[u].v[2 * t] = pack_f16(sc[u][t][0] * s[0], sc[u][t][1] * s[1]);
+                pp[u].v[2 * t + 1] = pack_f16(sc[u][t][2] * s[2], sc[u][t][3] * s[3]);
             }
         }
 #pragma unroll
@@ -604,6 +608,7 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
             for (int u = 0; u < RT; ++u) rows[u].o[n] = mf::mfma<DT_F16>(a, pp[u], rows[u].o[n]);
         }
     }
+    priority_rest(late);
 }
 
 // Puts the sums of `parts` parts, the first at byte `at0` and `stride` bytes
@@ -801,6 +806,9 @@ __global__ __launch_bounds__(64 * attend_waves(RT), attend_occupancy(D, RT)) voi
     }
     float ref_e = -100.0f;
 
+    // the second of the wavefronts, or workgroups, that share a SIMD
+    const bool late = kAttendWaves == 8 ? wave >= 4 : (blockIdx.x & 256) != 0;
+    priority_rest(late);
     int slot = 0, t = t0 + 32 * wave;
     auto turn = [&](auto edge) {
         // the slot that the step before this one was read from
@@ -815,7 +823,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT), attend_occupancy(D, RT)) voi
             if (after == 0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             else if (after == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L::kLoads) : "memory");
             else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * L::kLoads) : "memory");
-            step<DT, D, GS, RT, decltype(edge)::value>(ring + slot * L::kWords, rows, ref_e, lane, t - nt.pos0, t1 - t);
+            step<DT, D, GS, RT, decltype(edge)::value>(ring + slot * L::kWords, rows, ref_e, lane, t - nt.pos0, t1 - t, late);
         }
         slot = slot == kAttendSlots - 1 ? 0 : slot + 1;
         t += kStride;
