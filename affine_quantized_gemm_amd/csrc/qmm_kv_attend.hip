@@ -4,35 +4,45 @@
 namespace qmm {
 namespace kv {
 
-template <> AttendFn attend_fn<DT_F16, 64>(int, int);
-template <> AttendFn attend_fn<DT_F16, 128>(int, int);
-template <> AttendFn attend_fn<DT_F16, 256>(int, int);
-template <> AttendFn attend_fn<DT_BF16, 64>(int, int);
-template <> AttendFn attend_fn<DT_BF16, 128>(int, int);
-template <> AttendFn attend_fn<DT_BF16, 256>(int, int);
+template <> AttendFn attend_fn<DT_F16, 64>(int);
+template <> AttendFn attend_fn<DT_F16, 128>(int);
+template <> AttendFn attend_fn<DT_F16, 256>(int);
+template <> AttendFn attend_fn<DT_BF16, 64>(int);
+template <> AttendFn attend_fn<DT_BF16, 128>(int);
+template <> AttendFn attend_fn<DT_BF16, 256>(int);
 
 namespace {
 
+constexpr int kByRowsUpTo = 512;  // tokens
+
 struct AttendPlan {
     int row_tiles, row_groups, parts;
+    bool by_rows;
     int64_t bytes;
 };
 
-// Row tiles: 16 rows each, 1 or 2 a wavefront (heads of 256: 1, for the registers).
+// More than two tiles of rows go by rows over short sequences, where the work
+// of a workgroup's start and end counts: 17 sequences of 100 tokens, 53 rows
+// of each of 16 heads 13.5 us, by tokens 31.4.  Over long ones by tokens,
+// with two tiles a wavefront (heads of 256 have the registers for one) and
+// fewer rows to put together: 256 rows a head over 16k tokens 118 us, by rows
+// 142; 220 rows over 700 to 1414 tokens 27.9 us, by rows 34.4.
 // Parts for the workgroups that fill the chip over the kv heads and row
 // groups; where the sequences are that many, or short, or too many to plan,
 // one part each.
 AttendPlan plan_of(const qmm_kv_cache& c, int64_t seqs, int64_t max_new, int64_t heads, int64_t max_len) {
     AttendPlan p;
-    const int64_t rows = max_new * (heads / c.kv_heads);
-    p.row_tiles = rows <= 16 || c.head_dim == 256 ? 1 : 2;
-    p.row_groups = static_cast<int>((rows + 16 * p.row_tiles - 1) / (16 * p.row_tiles));
+    const int64_t tiles = (max_new * (heads / c.kv_heads) + 15) / 16;
+    const int64_t most_tiles = c.head_dim == 256 ? 1 : 2;
+    p.by_rows = tiles > most_tiles && max_len <= kByRowsUpTo;
+    p.row_tiles = tiles == 1 || most_tiles == 1 || (p.by_rows && tiles <= 4) ? 1 : 2;
+    const int per = attend_tiles(p.row_tiles, p.by_rows);
+    p.row_groups = static_cast<int>((tiles + per - 1) / per);
     const int64_t each = static_cast<int64_t>(c.kv_heads) * p.row_groups;
-    const int workgroups = attend_workgroups(p.row_tiles);
-    int64_t parts = workgroups / each;
+    int64_t parts = attend_workgroups(p.row_tiles) / each;
     const int64_t most = seqs * ((max_len + kChunk - 1) / kChunk);
     parts = parts < most ? parts : most;
-    if (parts <= seqs || seqs > 64 * kPlanLanes) parts = seqs;
+    if (p.by_rows || parts <= seqs || seqs > 64 * kPlanLanes) parts = seqs;
     p.parts = static_cast<int>(parts);
     // (sequences are cut only where seqs * each < workgroups: the counters fit their fixed place)
     static_assert(4 * kDoneStride * attend_workgroups(1) <= QMM_KV_ATTEND_ZEROED_BYTES, "a counter for each");
@@ -69,12 +79,12 @@ hipError_t launch_attend(const qmm_kv_cache& c, const AttendArgs& a) {
     AttendFn fn = nullptr;
     const bool half = c.dt == QMM_F16;
     switch (c.head_dim) {
-        case 64: fn = half ? attend_fn<DT_F16, 64>(c.group_size, p.row_tiles) : attend_fn<DT_BF16, 64>(c.group_size, p.row_tiles); break;
-        case 128: fn = half ? attend_fn<DT_F16, 128>(c.group_size, p.row_tiles) : attend_fn<DT_BF16, 128>(c.group_size, p.row_tiles); break;
-        case 256: fn = half ? attend_fn<DT_F16, 256>(c.group_size, p.row_tiles) : attend_fn<DT_BF16, 256>(c.group_size, p.row_tiles); break;
+        case 64: fn = half ? attend_fn<DT_F16, 64>(c.group_size) : attend_fn<DT_BF16, 64>(c.group_size); break;
+        case 128: fn = half ? attend_fn<DT_F16, 128>(c.group_size) : attend_fn<DT_BF16, 128>(c.group_size); break;
+        case 256: fn = half ? attend_fn<DT_F16, 256>(c.group_size) : attend_fn<DT_BF16, 256>(c.group_size); break;
         default: break;
     }
-    return fn != nullptr ? fn(k, grid, a.stream) : hipErrorInvalidValue;
+    return fn != nullptr ? fn(k, p.row_tiles, p.by_rows, grid, a.stream) : hipErrorInvalidValue;
 }
 
 }  // namespace kv

@@ -53,13 +53,19 @@ namespace kv {
 constexpr int kAttendSlots = 2;   // steps of a wavefront in LDS: one read, the others on their way
 constexpr float kFar = -3.0e38f;
 
-// Wavefronts of a workgroup, and how many a SIMD the registers are to leave
-// room for.  One row tile: workgroups of 4, for shorter parts.  Two: 8, half
-// as many parts to put together.
-constexpr int attend_waves(int row_tiles) { return row_tiles == 2 ? 8 : 4; }
+// How a workgroup's wavefronts share the work.  By tokens: all have the same
+// one or two row tiles, take the part's steps in turn and add up at the end
+// (one tile: 4 wavefronts, for shorter parts; two: 8, half as many parts to
+// put together).  By rows, where there are several tiles: 4 wavefronts have
+// one or two tiles of their own each and all the tokens of a sequence, and
+// nothing to add.
+constexpr int attend_waves(int row_tiles, bool by_rows) { return row_tiles == 2 && !by_rows ? 8 : 4; }
+// Rows of a workgroup, in tiles.
+constexpr int attend_tiles(int row_tiles, bool by_rows) { return by_rows ? 4 * row_tiles : row_tiles; }
+// Wavefronts a SIMD that the registers are to leave room for.
 constexpr int attend_occupancy(int dim, int row_tiles) { return dim == 256 || row_tiles == 2 ? 2 : 3; }
 // Workgroups that a call is cut into at most: 8 wavefronts a CU.
-constexpr int attend_workgroups(int row_tiles) { return 2048 / attend_waves(row_tiles); }
+constexpr int attend_workgroups(int row_tiles) { return 2048 / attend_waves(row_tiles, false); }
 
 // The tokens of a sequence are cut into parts of whole chunks, one workgroup
 // a part.
@@ -703,13 +709,11 @@ __device__ __forceinline__ void join_parts(Shared sums, uint32_t at0, uint32_t s
 
 }  // namespace
 
-// One workgroup: one part of one sequence and kv head against RT tiles of 16
-// rows (row = new token * group + head within the group).  Its four
-// wavefronts take the part's steps of 32 tokens in turn, each with sums of
-// its own, which are put together through LDS at the end.
-template <int DT, int D, int GS, int RT, bool NT_LOADS>
-__global__ __launch_bounds__(64 * attend_waves(RT), attend_occupancy(D, RT)) void attend_kernel(AttendParams a) {
-    constexpr int kAttendWaves = attend_waves(RT);
+// One workgroup: one part of one sequence and kv head against the rows of row
+// group blockIdx.y (row = new token * group + head within the group).
+template <int DT, int D, int GS, int RT, bool ROWS, bool NT_LOADS>
+__global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT)) void attend_kernel(AttendParams a) {
+    constexpr int kAttendWaves = attend_waves(RT, ROWS), kTiles = attend_tiles(RT, ROWS);
     using L = Slot<D, GS>;
     constexpr int G = D / GS, NT = D / 16;
     constexpr int DC = D < 128 ? D : 128;      // values a row that go through LDS at a time
@@ -729,7 +733,9 @@ __global__ __launch_bounds__(64 * attend_waves(RT), attend_occupancy(D, RT)) voi
     if (b < 0) return;
     const NewTokens nt = new_tokens(a.s, b);
     const int count = nt.n * static_cast<int>(a.group);
-    if (rg * 16 * RT >= count) return;
+    const int base_row = rg * 16 * kTiles;
+    if (base_row >= count) return;
+    const int wave_row = base_row + (ROWS ? wave * 16 * RT : 0);  // the wavefront's first
     const int64_t cap = a.s.width << a.s.page_shift;
     const int len = static_cast<int>(nt.pos0 + nt.n < cap ? nt.pos0 + nt.n : cap);
     const int t0 = part.first * kChunk;
@@ -756,7 +762,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT), attend_occupancy(D, RT)) voi
     uint64_t bits[RT];
 #pragma unroll
     for (int u = 0; u < RT; ++u) {
-        const int row = (rg * RT + u) * 16 + i;
+        const int row = wave_row + 16 * u + i;
         const bool have = row < count;
         const int tok = have ? static_cast<uint32_t>(row) / a.group : 0;
         const uint16_t* q = a.q + (nt.row0 + tok) * a.q_row +
@@ -776,7 +782,9 @@ __global__ __launch_bounds__(64 * attend_waves(RT), attend_occupancy(D, RT)) voi
     }
     uint32_t* ring = lds + wave * (kAttendSlots * L::kWords);
     const uint32_t ring_at = lds_address(ring);
-    constexpr int kStride = 32 * kAttendWaves;
+    constexpr int kStride = ROWS ? 32 : 32 * kAttendWaves;
+    // a wavefront without rows (by rows) takes no steps
+    const int t_first = ROWS ? (wave_row < count ? t0 : t1) : t0 + 32 * wave;
     // starts the loads of the step at token t; whether there are any
     auto fetch = [&](int t, int slot) -> bool {
         if (t >= t1) return false;
@@ -790,7 +798,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT), attend_occupancy(D, RT)) voi
     unsigned there = 0;
 #pragma unroll
     for (int n = 0; n < kAttendSlots - 1; ++n)
-        there |= fetch(t0 + 32 * wave + n * kStride, n) ? 1u << n : 0u;
+        there |= fetch(t_first + n * kStride, n) ? 1u << n : 0u;
     RowTile<D, GS> rows[RT];
 #pragma unroll
     for (int u = 0; u < RT; ++u) {
@@ -809,7 +817,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT), attend_occupancy(D, RT)) voi
     // the second of the wavefronts, or workgroups, that share a SIMD
     const bool late = kAttendWaves == 8 ? wave >= 4 : (blockIdx.x & 256) != 0;
     priority_rest(late);
-    int slot = 0, t = t0 + 32 * wave;
+    int slot = 0, t = t_first;
     auto turn = [&](auto edge) {
         // the slot that the step before this one was read from
         const int free_slot = slot == 0 ? kAttendSlots - 1 : slot - 1;
@@ -832,7 +840,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT), attend_occupancy(D, RT)) voi
     const int seen = nt.pos0 < t1 ? nt.pos0 : t1;
     while (t + 32 <= seen) turn(std::false_type{});
     while (t < t1) turn(std::true_type{});
-    __syncthreads();  // the slots become the sums' buffer
+    if constexpr (!ROWS) __syncthreads();  // the slots become the sums' buffer
 
     // one set of sums: R and l first
     float bias[RT][G];
@@ -843,18 +851,17 @@ __global__ __launch_bounds__(64 * attend_waves(RT), attend_occupancy(D, RT)) voi
 #pragma unroll
         for (int g = 0; g < G; ++g)
             bias[u][g] = __shfl(rows[u].zb[g % 4], i + 16 * (g / 4)) + 7.5f * __shfl(rows[u].zb[g % 4], i + 16 * (2 + g / 4));
-        if (j == 0) {
+        if (!ROWS && j == 0) {
             stat[wave][u][i][0] = rows[u].l > 0.0f ? rows[u].m + ref_e : kFar;
             stat[wave][u][i][1] = rows[u].l;
         }
     }
-    __syncthreads();
+    if constexpr (!ROWS) __syncthreads();
     uint32_t* done = a.done + kDoneStride * ((static_cast<int64_t>(b) * gridDim.y + rg) * a.s.kv_heads + head);
     const Shared sums = shared_of(a.sums);
     auto sums_at = [&](int slot) -> uint32_t {  // (all parts' sums are some tens of MB)
         return ((static_cast<uint32_t>(slot) * gridDim.y + rg) * a.s.kv_heads + head) * (4 * part_floats(D, RT));
     };
-    const int base_row = rg * 16 * RT;
     constexpr int PER = DC * 16 / (64 * kAttendWaves) > 4 ? DC * 16 / (64 * kAttendWaves) : 4;
     const int oi = threadIdx.x / (DC / PER) % 16, dd = threadIdx.x % (DC / PER) * PER;
     // one row's values, normalized and rounded
@@ -874,61 +881,80 @@ __global__ __launch_bounds__(64 * attend_waves(RT), attend_occupancy(D, RT)) voi
         if (a.lse != nullptr)
             a.lse[at] = l > 0.0f ? 0.693147180559945f * (ref + __builtin_amdgcn_logf(l)) : -__builtin_inff();
     };
+    // value 16 n + 4 j + r of a row, from its three sums
+    auto value = [&](int u, int n, int r) {
+        const float up = (n & 1) ? 0x1p20f : 0x1p24f;
+        return __builtin_fmaf(rows[u].o[n][r], up, bias[u][16 * n / GS]) - 7.5f * rows[u].z[16 * n / GS][r];
+    };
+    if constexpr (ROWS) {
 #pragma unroll
-    for (int u = 0; u < RT; ++u) {
-        float ref = kFar;
+        for (int u = 0; u < RT; ++u) {
+            const int row = wave_row + 16 * u + i;
+            if (row >= count) continue;
+            const float l = rows[u].l, inv = l > 0.0f ? 1.0f / l : 0.0f;
+            const int64_t at = out_at(row);
 #pragma unroll
-        for (int w = 0; w < kAttendWaves; ++w) ref = fmaxf(ref, stat[w][u][i][0]);
-        // (a wavefront that saw nothing has l = 0 and sums of 0)
-        const float f = rows[u].l > 0.0f ? exp2_fast(rows[u].m + ref_e - ref) : 0.0f;
-        const int out_row = base_row + 16 * u + oi;
-#pragma unroll
-        for (int d0 = 0; d0 < D; d0 += DC) {
-#pragma unroll
-            for (int n = d0 / 16; n < (d0 + DC) / 16; ++n) {
-                const int g = 16 * n / GS;
-                const float up = (n & 1) ? 0x1p20f : 0x1p24f;
-                float4_t v;
-#pragma unroll
-                for (int r2 = 0; r2 < 4; ++r2)
-                    v[r2] = f * (__builtin_fmaf(rows[u].o[n][r2], up, bias[u][g]) - 7.5f * rows[u].z[g][r2]);
-                *reinterpret_cast<float4_t*>(&buf[wave][i * kRow + 16 * n - d0 + 4 * j]) = v;
+            for (int n = 0; n < NT; ++n) {
+                const float o[4] = {value(u, n, 0), value(u, n, 1), value(u, n, 2), value(u, n, 3)};
+                put(at, 16 * n + 4 * j, o, inv);
             }
-            __syncthreads();
-            // a thread takes PER values of a row
-            float o[PER];
+            if (j == 0) put_lse(at, rows[u].m + ref_e, l);
+        }
+        return;  // (a sequence is one part)
+    } else {
 #pragma unroll
-            for (int e = 0; e < PER; ++e) o[e] = 0.0f;
+        for (int u = 0; u < RT; ++u) {
+            float ref = kFar;
 #pragma unroll
-            for (int w = 0; w < kAttendWaves; ++w)
+            for (int w = 0; w < kAttendWaves; ++w) ref = fmaxf(ref, stat[w][u][i][0]);
+            // (a wavefront that saw nothing has l = 0 and sums of 0)
+            const float f = rows[u].l > 0.0f ? exp2_fast(rows[u].m + ref_e - ref) : 0.0f;
+            const int out_row = base_row + 16 * u + oi;
 #pragma unroll
-                for (int e = 0; e < PER; e += 4) {
-                    const float4_t v = *reinterpret_cast<const float4_t*>(&buf[w][oi * kRow + dd + e]);
+            for (int d0 = 0; d0 < D; d0 += DC) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) o[e + k] += v[k];
+                for (int n = d0 / 16; n < (d0 + DC) / 16; ++n) {
+                    float4_t v;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[r] = f * value(u, n, r);
+                    *reinterpret_cast<float4_t*>(&buf[wave][i * kRow + 16 * n - d0 + 4 * j]) = v;
                 }
-            float big = kFar, l = 0.0f;
+                __syncthreads();
+                // a thread takes PER values of a row
+                float o[PER];
 #pragma unroll
-            for (int w = 0; w < kAttendWaves; ++w) big = fmaxf(big, stat[w][u][oi][0]);
+                for (int e = 0; e < PER; ++e) o[e] = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kAttendWaves; ++w)
-                l += stat[w][u][oi][1] > 0.0f ? stat[w][u][oi][1] * exp2_fast(stat[w][u][oi][0] - big) : 0.0f;
-            if (out_row < count && threadIdx.x < 16 * DC / PER) {
-                if (part.parts == 1) {
-                    const int64_t at = out_at(out_row);
+                for (int w = 0; w < kAttendWaves; ++w)
 #pragma unroll
-                    for (int e = 0; e < PER; e += 4) put(at, d0 + dd + e, o + e, l > 0.0f ? 1.0f / l : 0.0f);
-                    if (d0 == 0 && dd == 0) put_lse(at, big, l);
-                } else {
-                    const uint32_t at = sums_at(part.slot0 + part.part);
+                    for (int e = 0; e < PER; e += 4) {
+                        const float4_t v = *reinterpret_cast<const float4_t*>(&buf[w][oi * kRow + dd + e]);
 #pragma unroll
-                    for (int e = 0; e < PER; e += 4)
-                        store_shared(sums, at + 4 * ((16 * u + oi) * D + d0 + dd + e), float4_t{o[e], o[e + 1], o[e + 2], o[e + 3]});
-                    if (d0 == 0 && dd == 0)
-                        store_shared(sums, at + 4 * (16 * RT * D + 4 * (16 * u + oi)), float4_t{l > 0.0f ? big : kFar, l, 0.0f, 0.0f});
+                        for (int k = 0; k < 4; ++k) o[e + k] += v[k];
+                    }
+                float big = kFar, l = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kAttendWaves; ++w) big = fmaxf(big, stat[w][u][oi][0]);
+#pragma unroll
+                for (int w = 0; w < kAttendWaves; ++w)
+                    l += stat[w][u][oi][1] > 0.0f ? stat[w][u][oi][1] * exp2_fast(stat[w][u][oi][0] - big) : 0.0f;
+                if (out_row < count && threadIdx.x < 16 * DC / PER) {
+                    if (part.parts == 1) {
+                        const int64_t at = out_at(out_row);
+#pragma unroll
+                        for (int e = 0; e < PER; e += 4) put(at, d0 + dd + e, o + e, l > 0.0f ? 1.0f / l : 0.0f);
+                        if (d0 == 0 && dd == 0) put_lse(at, big, l);
+                    } else {
+                        const uint32_t at = sums_at(part.slot0 + part.part);
+#pragma unroll
+                        for (int e = 0; e < PER; e += 4)
+                            store_shared(sums, at + 4 * ((16 * u + oi) * D + d0 + dd + e), float4_t{o[e], o[e + 1], o[e + 2], o[e + 3]});
+                        if (d0 == 0 && dd == 0)
+                            store_shared(sums, at + 4 * (16 * RT * D + 4 * (16 * u + oi)), float4_t{l > 0.0f ? big : kFar, l, 0.0f, 0.0f});
+                    }
                 }
+                __syncthreads();
             }
-            __syncthreads();
         }
     }
     if (part.parts == 1) return;
@@ -939,7 +965,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT), attend_occupancy(D, RT)) voi
     // behind a device fence write back and drop the whole L2 for every
     // workgroup: 75 us more for 512 of them.)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
+    __syncthreads();  // (also: no slot is read or written any more)
     uint32_t* flag = lds;
     if (threadIdx.x == 0) {
         const uint32_t n = __hip_atomic_fetch_add(done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -965,51 +991,56 @@ __global__ __launch_bounds__(64 * attend_waves(RT), attend_occupancy(D, RT)) voi
     else join_parts<D, RT, W, 1, 12>(sums, at0, stride, part.parts, valid, meet, finish);
 }
 
-template <int DT, int D, int GS, int RT, bool NT_LOADS>
+template <int DT, int D, int GS, int RT, bool ROWS, bool NT_LOADS>
 hipError_t launch_attend_kernel(const AttendParams& p, dim3 grid, hipStream_t st) {
-    constexpr int kAttendWaves = attend_waves(RT);
+    constexpr int W = attend_waves(RT, ROWS);
     constexpr int kRow = (D < 128 ? D : 128) + 4;
-    constexpr int slots = 4 * kAttendWaves * kAttendSlots * Slot<D, GS>::kWords;
-    constexpr int sums = 4 * kAttendWaves * (16 * kRow + RT * 16 * 2);
+    constexpr int slots = 4 * W * kAttendSlots * Slot<D, GS>::kWords;
+    constexpr int sums = 4 * W * (16 * kRow + RT * 16 * 2);
     constexpr int bytes = slots > sums ? slots : sums;
     if constexpr (bytes > 64 * 1024) {
         static std::atomic<uint64_t> raised{0};
         const hipError_t e =
-            raise_lds_limit(reinterpret_cast<const void*>(&attend_kernel<DT, D, GS, RT, NT_LOADS>), raised);
+            raise_lds_limit(reinterpret_cast<const void*>(&attend_kernel<DT, D, GS, RT, ROWS, NT_LOADS>), raised);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((attend_kernel<DT, D, GS, RT, NT_LOADS>), grid, dim3(64 * kAttendWaves), bytes, st, p);
+    hipLaunchKernelGGL((attend_kernel<DT, D, GS, RT, ROWS, NT_LOADS>), grid, dim3(64 * W), bytes, st, p);
     return hipGetLastError();
 }
 
-template <int DT, int D, int GS, int RT>
-hipError_t run_attend(const AttendParams& p, dim3 grid, hipStream_t st) {
-    // tokens that several workgroups read stay in L2
-    if constexpr (RT > 1 || D == 256)
-        if (grid.y > 1) return launch_attend_kernel<DT, D, GS, RT, false>(p, grid, st);
-    return launch_attend_kernel<DT, D, GS, RT, true>(p, grid, st);
+// Tokens that several wavefronts or workgroups read stay in L2; others are
+// streamed past it.
+template <int DT, int D, int GS>
+hipError_t run_attend(const AttendParams& p, int row_tiles, bool by_rows, dim3 grid, hipStream_t st) {
+    if constexpr (D <= 128) {
+        if (row_tiles == 2 && by_rows) return launch_attend_kernel<DT, D, GS, 2, true, false>(p, grid, st);
+        if (row_tiles == 2 && grid.y > 1) return launch_attend_kernel<DT, D, GS, 2, false, false>(p, grid, st);
+        if (row_tiles == 2) return launch_attend_kernel<DT, D, GS, 2, false, true>(p, grid, st);
+    }
+    if (by_rows) return launch_attend_kernel<DT, D, GS, 1, true, false>(p, grid, st);
+    if constexpr (D == 256)
+        if (grid.y > 1) return launch_attend_kernel<DT, D, GS, 1, false, false>(p, grid, st);
+    return launch_attend_kernel<DT, D, GS, 1, false, true>(p, grid, st);
 }
 
 // One translation unit per type and head size.
-using AttendFn = hipError_t (*)(const AttendParams&, dim3, hipStream_t);
+using AttendFn = hipError_t (*)(const AttendParams&, int row_tiles, bool by_rows, dim3, hipStream_t);
 template <int DT, int D>
-AttendFn attend_fn(int gs, int row_tiles);
+AttendFn attend_fn(int gs);
 
 }  // namespace kv
 }  // namespace qmm
 
-// Instantiates attend_fn<DT, D> for 1 or (heads up to 128) 2 row tiles.
-#define QMM_KV_ATTEND_GS(DTV, DV, GSV) \
-    if (gs == GSV) return row_tiles == 1 ? run_attend<DTV, DV, GSV, 1> : run_attend<DTV, DV, GSV, DV == 256 ? 1 : 2>
-#define QMM_KV_ATTEND_UNIT(DTV, DV)                                         \
-    namespace qmm {                                                         \
-    namespace kv {                                                          \
-    template <>                                                             \
-    AttendFn attend_fn<DTV, DV>(int gs, int row_tiles) {                    \
-        QMM_KV_ATTEND_GS(DTV, DV, 32);                                      \
-        QMM_KV_ATTEND_GS(DTV, DV, 64);                                      \
-        if constexpr (DV >= 128) QMM_KV_ATTEND_GS(DTV, DV, 128);            \
-        return nullptr;                                                     \
-    }                                                                       \
-    }                                                                       \
+#define QMM_KV_ATTEND_UNIT(DTV, DV)                             \
+    namespace qmm {                                             \
+    namespace kv {                                              \
+    template <>                                                 \
+    AttendFn attend_fn<DTV, DV>(int gs) {                       \
+        if (gs == 32) return run_attend<DTV, DV, 32>;           \
+        if (gs == 64) return run_attend<DTV, DV, 64>;           \
+        if constexpr (DV >= 128)                                \
+            if (gs == 128) return run_attend<DTV, DV, 128>;     \
+        return nullptr;                                         \
+    }                                                           \
+    }                                                           \
     }

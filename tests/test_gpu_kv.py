@@ -206,6 +206,20 @@ def test_attend_long(Q, dt, rows):
     assert a.shape == (4 * rows, 2, 128)
 
 
+@pytest.mark.parametrize("dt,dim,gs,heads,rows", [
+    ("f16", 128, 64, 10, 5), ("bf16", 64, 32, 6, 7), ("f16", 64, 64, 3, 14),  # 3 and 4 tiles of rows over long sequences
+    ("bf16", 128, 128, 5, 20), ("f16", 128, 32, 9, 33), ("bf16", 256, 64, 3, 30),  # more
+])
+def test_attend_many_rows_long(Q, dt, dim, gs, heads, rows):
+    """Ragged rows that leave tiles, wavefronts and workgroups without any, over long sequences and short ones."""
+    print(f"attend {dt} D={dim} gs={gs} heads={heads} rows={rows}", flush=True)
+    new = np.array([rows, 1, rows // 2, rows])
+    lens = np.array([1600, 1100, rows, 300])
+    c, tables = filled(dt, dim, gs, 64, 1, lens, 26, 56, 95)
+    check_attend(Q, c, tables, lens, new, heads, 96)
+    check_attend(Q, c, tables, lens, new, heads, 96, max_len=900)
+
+
 def test_attend_masks(Q):
     """Draft trees; rows that see only what was before, or nothing at all."""
     rng = np.random.default_rng(1)
