@@ -13,20 +13,23 @@ template <> AttendFn attend_fn<DT_BF16, 256>(int);
 
 namespace {
 
-constexpr int kByRowsUpTo = 512;  // tokens
-
 struct AttendPlan {
     int row_tiles, row_groups, parts;
     bool by_rows;
     int64_t bytes;
 };
 
-// More than two tiles of rows go by rows over short sequences, where the work
-// of a workgroup's start and end counts: 17 sequences of 100 tokens, 53 rows
-// of each of 16 heads 13.5 us, by tokens 31.4.  Over long ones by tokens,
-// with two tiles a wavefront (heads of 256 have the registers for one) and
-// fewer rows to put together: 256 rows a head over 16k tokens 118 us, by rows
-// 142; 220 rows over 700 to 1414 tokens 27.9 us, by rows 34.4.
+// By tokens, with two tiles of rows a wavefront (heads of 256 have the
+// registers for one), or where there are more tiles by rows, a workgroup a
+// sequence.  By rows costs the tokens of a sequence one after another, by
+// tokens a start, a meeting of its wavefronts and an end for every two tiles:
+// over sequences, kv heads and pairs of tiles, as multiples of the
+// workgroups that the chip runs at a time, those weigh as
+// 512 * multiple > max_len + 384.  Measured (us, by rows / by tokens, 64
+// rows of 4 heads of 128): multiple 1/16, 512 tokens 20.7 / 14.4; 1, 128
+// 10.4 / 11.4 and 512 22.0 / 13.9; 2, 128 10.8 / 20.9, 512 22.7 / 26.2 and
+// 1024 38.9 / 33.2; 4, 1024 43.3 / 64.8 and 4096 143 / 144.  64 rows of 32
+// heads over 16k tokens 142 / 118.
 // Parts for the workgroups that fill the chip over the kv heads and row
 // groups; where the sequences are that many, or short, or too many to plan,
 // one part each.
@@ -34,7 +37,8 @@ AttendPlan plan_of(const qmm_kv_cache& c, int64_t seqs, int64_t max_new, int64_t
     AttendPlan p;
     const int64_t tiles = (max_new * (heads / c.kv_heads) + 15) / 16;
     const int64_t most_tiles = c.head_dim == 256 ? 1 : 2;
-    p.by_rows = tiles > most_tiles && max_len <= kByRowsUpTo;
+    const int64_t units = seqs * c.kv_heads * ((tiles + most_tiles - 1) / most_tiles);
+    p.by_rows = tiles > most_tiles && max_len + 384 <= 512 * units / attend_workgroups(static_cast<int>(most_tiles));
     p.row_tiles = tiles == 1 || most_tiles == 1 || (p.by_rows && tiles <= 4) ? 1 : 2;
     const int per = attend_tiles(p.row_tiles, p.by_rows);
     p.row_groups = static_cast<int>((tiles + per - 1) / per);

@@ -151,9 +151,10 @@ class KVCache:
             return torch._C._cuda_getCurrentRawStream(self.device.index)
         return int(getattr(stream, "cuda_stream", stream))
 
-    def attend_workspace(self, seqs: int, max_new: int, rows: int, heads: int, max_len: int) -> torch.Tensor:
-        """A workspace for :meth:`attend` calls of up to these sizes (one per stream, or per captured graph)."""
-        need = self.attend_workspace_bytes(seqs, max_new, rows, heads, max_len)
+    def attend_workspace(self, *sizes: int) -> torch.Tensor:
+        """A workspace for :meth:`attend` calls (one per stream, or per captured graph): of the sizes given, as in
+        :meth:`attend_workspace_bytes`, or without them of any sizes.  (Fewer sequences can need more.)"""
+        need = self.attend_workspace_bytes(*sizes) if sizes else self._most_space
         return torch.zeros((max(need, 16),), dtype=torch.uint8, device=self.device)
 
     def _kept_space(self, stream, raw: int):

@@ -419,9 +419,10 @@ int qmm_kv_read(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_
  *     new tokens j whose bit j is set in the row's word (a draft tree: the
  *     row's own token and its ancestors).
  *   - A row that sees nothing gives zeros and lse = -infinity.
- * fp32 accumulation, softmax and sums; k_hat and v_hat are not rounded; the
- * probabilities (times the scale of their value) are rounded to dt for the
- * second product; one rounding to dt at the end.  Deterministic.
+ * fp32 accumulation, softmax and sums; k_hat and v_hat are not rounded; for
+ * the second product the probabilities times the scale of their value are
+ * rounded to fp16 (11 bits, either dt), for the biases to dt; one rounding to
+ * dt at the end.  Deterministic.
  *
  * max_len: no sequence is longer (1..table_width * page_size); it bounds how
  * many parts the sequences are cut into.  Longer ones are still attended to
@@ -431,8 +432,8 @@ int qmm_kv_read(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_
  * other arrays.  Its first QMM_KV_ATTEND_ZEROED_BYTES bytes must be zero
  * before the first call that uses it; every call leaves them zero (calls of
  * any sizes may follow each other on one workspace).  Two calls in flight
- * need two.  No call needs more than QMM_KV_ATTEND_ZEROED_BYTES + 32768 *
- * (head_dim + 4) bytes.
+ * need two.  Fewer sequences or tokens can need more; no call needs more
+ * than QMM_KV_ATTEND_ZEROED_BYTES + 32768 * (head_dim + 4) bytes.
  * heads < 1, or not a multiple of kv_heads, max_new > 64 ->
  * QMM_ERR_UNSUPPORTED.
  */

@@ -220,6 +220,82 @@ def test_attend_many_rows_long(Q, dt, dim, gs, heads, rows):
     check_attend(Q, c, tables, lens, new, heads, 96, max_len=900)
 
 
+@pytest.mark.parametrize("dt,dim,gs,kv_heads,group,rows,longest", [
+    ("f16", 128, 64, 8, 1, 64, 40), ("bf16", 64, 32, 7, 3, 20, 150),  # 4 tiles of rows a sequence
+    ("f16", 64, 64, 8, 5, 9, 260), ("bf16", 128, 32, 5, 7, 31, 129),  # 3, and 14
+    ("bf16", 256, 64, 4, 3, 30, 70), ("f16", 256, 128, 8, 1, 33, 33),  # heads of 256: 6 and 3
+])
+def test_attend_many_rows_and_sequences(Q, dt, dim, gs, kv_heads, group, rows, longest):
+    """Enough sequences for workgroups by rows; ragged ends of both, empty sequences, draft trees."""
+    print(f"attend {dt} D={dim} gs={gs} kv_heads={kv_heads} group={group} rows={rows}", flush=True)
+    rng = np.random.default_rng(7)
+    seqs = 48
+    new = rng.integers(0, rows + 1, seqs)
+    new[:6] = rows, 1, rows, 0, 0, rows
+    lens = np.maximum(new, rng.integers(0, longest + 1, seqs))
+    lens[:6] = max(rows, longest), 1, rows, 0, longest, 32 * -(-rows // 32)
+    width = -(-int(lens.max()) // 64) + 1
+    c, tables = filled(dt, dim, gs, 64, kv_heads, lens, width, int((-(-lens // 64)).sum()) + 2, 97)
+    most = int(lens.max())
+    check_attend(Q, c, tables, lens, new, group * kv_heads, 98, max_len=most)
+    masks = rng.integers(0, 1 << 62, int(new.sum())) * rng.integers(0, 2, int(new.sum()))
+    check_attend(Q, c, tables, lens, new, group * kv_heads, 98, mask=masks, max_len=most)
+
+
+def test_attend_many_sequences(Q):
+    """More sequences than are planned over: one part each, however long."""
+    rng = np.random.default_rng(8)
+    lens = rng.integers(1, 40, 300)
+    lens[[0, 257]] = 900, 1300
+    c, tables = filled("f16", 64, 32, 32, 1, lens, 41, int((-(-lens // 32)).sum()), 99)
+    check_attend(Q, c, tables, lens, np.ones(300, int), 4, 100)
+
+
+def test_pool_beyond_32_bits(Q):
+    """Pages whose words lie past 2^31 bytes, 2^32 bytes and 2^31 words: append, read, attend, copy."""
+    lens, new, pages = np.array([300, 513, 256]), np.array([3, 1, 5]), 13200
+    c, tables = filled("f16", 256, 32, 256, 8, lens, 3, 6, 101)
+    small = gpu_cache(Q, c)
+    big = Q.KVCache.empty(1, pages, 8, 256, 32, 256)
+    assert big.pool.numel() > 2 ** 31
+    place = torch.tensor([pages - 1, 4000, 7000, pages - 2, 9000, pages - 7], device="cuda")
+    big.pool[:, place] = small.pool
+    far = torch.where(i32(tables) < 0, i32(tables), place.to(torch.int32)[i32(tables).long()])
+    starts = np.concatenate([[0], np.cumsum(new)])
+    kw = {"starts": i32(starts), "max_new": 5}
+    k, v, q = (values(9, h, 256, "f16", 102 + h).cuda() for h in (8, 8, 16))
+    got = []
+    for cache, t in ((small, i32(tables)), (big, far)):
+        cache.append(0, k, v, t, i32(lens), **kw)
+        got.append((*cache.read(0, 9, t, i32(lens), **kw), cache.attend(0, q, t, i32(lens), **kw)))
+    for a, b in zip(*got):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    assert torch.equal(big.pool[:, place], small.pool)
+    big.copy_pages(i32([pages - 1, 4000]), i32([4001, pages - 3]))
+    assert torch.equal(big.pool[:, [4001, pages - 3]], small.pool[:, :2])
+
+
+def test_attend_on_two_streams(Q):
+    """Calls in flight on two streams, each cut into parts with counters of its own."""
+    lens = np.array([1536])
+    c, tables = filled("f16", 128, 64, 64, 2, lens, 24, 24, 110)
+    cache = gpu_cache(Q, c)
+    t = [i32(tables), i32(tables[:, ::-1].copy())]
+    n = i32(lens)
+    q = [synth.normal((1, 8, 128), 1.0, "f16", 112 + i).cuda() for i in range(2)]
+    want = [cache.attend(0, q[i], t[i], n) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(cache.attend(0, q[i], t[i], n))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g.view(torch.int16), want[i].view(torch.int16)) for g in got[i])
+
+
 def test_attend_masks(Q):
     """Draft trees; rows that see only what was before, or nothing at all."""
     rng = np.random.default_rng(1)
@@ -328,6 +404,31 @@ def test_step_in_a_graph(Q):
         torch.cuda.synchronize()
         assert torch.equal(graph_cache.pool, eager.pool)
         assert torch.equal(out.view(torch.int16), want.view(torch.int16)), t
+
+
+def test_graph_without_a_given_workspace(Q):
+    """A captured call that is cut into parts brings its own zeroed workspace; eager calls go on between replays."""
+    lens = np.array([1000, 1040])
+    c, tables = filled("bf16", 128, 64, 64, 2, lens, 18, 33, 145)
+    cache = gpu_cache(Q, c)
+    t, n = i32(tables), i32(lens)
+    q = torch.zeros(2, 8, 128, dtype=torch.bfloat16, device="cuda")
+    assert cache.attend_workspace_bytes(2, 1, 2, 8, 18 * 64) > 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        cache.attend(0, q, t, n)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = cache.attend(0, q, t, n)
+    for r in range(6):
+        q.copy_(synth.normal(tuple(q.shape), 1.0, "bf16", 146 + r))
+        n.copy_(i32([1000 - 130 * r, 40 + 200 * r]))
+        g.replay()
+        want = cache.attend(0, q, t, n)
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16)), r
 
 
 def test_python_refusals(Q):
