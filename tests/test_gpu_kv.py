@@ -579,3 +579,34 @@ def test_forked_sequences_attend_alike_and_then_apart(Q):
     assert (kb - k).abs().max() < 0.5 and (vb - v).abs().max() < 0.5
     cache.free(tables, lens, refs, i32([0, 1, 2]))
     assert refs.tolist() == [0] * 16 and lens.tolist() == [0, 0, 0] and (tables == -1).all()
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_speculative_decoding_example(Q, dt):
+    """Forked sequences, draft trees, cut back lengths, freed and compacted pages: every token that came out is the
+    likeliest one of a plain pass over its whole text.
+
+    Both passes quantize keys and values that differ by roundings, so a code may be the neighbour: a step of about
+    0.4 standard deviations in one of 128 values moves a score by 0.4 / sqrt(128) = 0.035, and as much of one
+    token's share of the sums; over both layers the logits move by well under a tenth of their deviation."""
+    from affine_quantized_gemm_amd import spec_decode as S
+    print(f"speculative decoding {dt}", flush=True)
+    model = S.Decoder(layers=2, hidden=512, heads=4, kv_heads=2, head_dim=128, ffn=512, vocab=512, dtype=DT[dt])
+    s = S.Sequences(model, 3, 70 + 1 + 45 * 7, 3)
+    prompt = torch.randint(0, 512, (70,), generator=torch.Generator().manual_seed(1)).cuda()
+    s.fork(s.prefill(prompt)[-1])
+    for _ in range(25):
+        s.step()
+    ended = s.texts()
+    s.end([1])
+    assert s.refs[:int((s.refs > 0).sum())].min() > 0  # the live pages are the lowest
+    for _ in range(15):
+        s.step()
+    texts = s.texts()
+    assert len(texts) == 2 and texts[0][:len(ended[0])] == ended[0] and texts[1][:len(ended[2])] == ended[2]
+    assert len({e[70] for e in ended}) == 3
+    assert sum(len(t) - 71 for t in texts) > 2 * 40 * 1.5  # drafts were accepted
+    for text in [*texts, ended[1]]:
+        logits = S.logits_of(model, text[:-1])[70:].float()
+        got = logits.gather(1, torch.tensor(text[71:], device="cuda")[:, None])[:, 0]
+        assert ((logits.amax(1) - got) <= 0.1 * logits.std(1)).all()
