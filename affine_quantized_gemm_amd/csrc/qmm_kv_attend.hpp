@@ -13,14 +13,19 @@
 // the vector ALUs bound this kernel.  The codes are centred because P' is
 // rounded to 11 bits: its error is then weighed by |c - 7.5|, about the size of
 // the values, and not by c; the centring itself is -7.5 sum_t P', a product
-// with ones.  R = M + E is a running reference: M follows
+// with a constant.  R = M + E is a running reference: M follows
 // the scores' maximum and E the exponent of the largest s_V, so that P' stays
 // near 1 whatever the values' size.  Both are moved (and everything summed so
 // far scaled) only when a score passes M by 8, or a scale 2^E by 2^7.
 //
 // Codes as operands.  A 4-bit code in the low bits of an fp16 is the
 // subnormal number c 2^-24 (in bits 4..7: 16 c 2^-24), which the matrix core
-// multiplies exactly: unpacking a word of 8 codes takes four ands and a
+// multiplies exactly.  But it cuts the products of a sum off at a distance
+// from the largest one's exponent, and all subnormals have -14: up to 2^-18 of
+// P' is lost from every even code's product, downwards.  So what these sums
+// are centred by is summed in the same form, over the codes 8..15, and loses
+// as much.  (Without, the average of 16k tokens is 1e-4 of itself off, half of
+// fp16's rounding.)  Unpacking a word of 8 codes takes four ands and a
 // shift, no conversion and no offset to take away again.  The factors 2^24
 // go into the scores' scale and the last step; the 16 of the odd codes into
 // the d order of Q (q / 16) and into the last step.  Q is scaled per row by a
@@ -333,7 +338,7 @@ struct RowTile {
     float cs;         // score -> log2 units
     float m, l;       // M; this lane's share of the sum of p
     float4_t zb;      // sums p b (rows 0..7: group) and p s (rows 8..15)
-    float4_t z[G];    // sum P'
+    float4_t z[G];    // lanes j = 0, 1: sum P'; 2, 3: 4 j + r times it, as a code
     float4_t o[NT];
     uint64_t bits;    // new tokens that the row sees
 };
@@ -577,8 +582,9 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
     }
     priority_products();
     // P' and the second product: tile n = 4 c + q of 16 d, from nibble q of the words of quad c
+    // (rows 0..7 of the constant: 1, rows 8..15: the codes 8..15)
     Frag ones;
-    ones.v[0] = ones.v[1] = ones.v[2] = ones.v[3] = 0x3C003C00u;
+    ones.v[0] = ones.v[1] = ones.v[2] = ones.v[3] = i < 8 ? 0x3C003C00u : 0x00010001u * i;
     uint32_t v[2][S];
 #pragma unroll
     for (int t = 0; t < 2; ++t) load_words<S>(x + L::kV + t * (L::kCodes / 2) + 16 * S * j + S * i, v[t]);
@@ -843,14 +849,23 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
     if constexpr (!ROWS) __syncthreads();  // the slots become the sums' buffer
 
     // one set of sums: R and l first
-    float bias[RT][G];
+    float bias[RT][G][2], centre[RT][G][2];
 #pragma unroll
     for (int u = 0; u < RT; ++u) {
         rows[u].l = sum_j(rows[u].l);
-        // sum p (b + 7.5 s) of group g: rows g and 8 + g of zb, in the lanes j = g / 4 and 2 + g / 4
 #pragma unroll
-        for (int g = 0; g < G; ++g)
-            bias[u][g] = __shfl(rows[u].zb[g % 4], i + 16 * (g / 4)) + 7.5f * __shfl(rows[u].zb[g % 4], i + 16 * (2 + g / 4));
+        for (int g = 0; g < G; ++g) {
+            // sum p (b + 7.5 s) of group g: rows g and 8 + g of zb, in the lanes j = g / 4 and 2 + g / 4
+            const float mid = __shfl(rows[u].zb[g % 4], i + 16 * (g / 4)) + 7.5f * __shfl(rows[u].zb[g % 4], i + 16 * (2 + g / 4));
+            // what the sums of codes are centred by: odd codes by 7.5 sum P',
+            // even ones by the mean of 8..15 times it, less 4 of it
+            const float4_t z = rows[u].z[g];
+            const float codes = z[0] + z[1] + z[2] + z[3], one = __shfl(z[0], i);
+            centre[u][g][0] = 0.125f * (__shfl(codes, i + 32) + __shfl(codes, i + 48));
+            centre[u][g][1] = (7.5f * 0x1p-20f) * one;
+            bias[u][g][0] = __builtin_fmaf(4.0f, one, mid);
+            bias[u][g][1] = mid;
+        }
         if (!ROWS && j == 0) {
             stat[wave][u][i][0] = rows[u].l > 0.0f ? rows[u].m + ref_e : kFar;
             stat[wave][u][i][1] = rows[u].l;
@@ -884,7 +899,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
     // value 16 n + 4 j + r of a row, from its three sums
     auto value = [&](int u, int n, int r) {
         const float up = (n & 1) ? 0x1p20f : 0x1p24f;
-        return __builtin_fmaf(rows[u].o[n][r], up, bias[u][16 * n / GS]) - 7.5f * rows[u].z[16 * n / GS][r];
+        return __builtin_fmaf(rows[u].o[n][r] - centre[u][16 * n / GS][n & 1], up, bias[u][16 * n / GS][n & 1]);
     };
     if constexpr (ROWS) {
 #pragma unroll
