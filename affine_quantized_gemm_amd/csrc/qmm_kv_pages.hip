@@ -49,7 +49,9 @@ struct Pool {
 };
 
 // One workgroup's share of moving `count` pages in every layer: pieces of
-// kMove * kPiece * 16 bytes.
+// kMove * kPiece * 16 bytes.  Bound by memory: 460 pages of 8 layers (543 MB
+// read and written) 101 us, 5.4 TB/s; three pages of one layer 3.0 us, which is
+// the launch and two dependent reads.
 __device__ void move_pages(const Pool& pool, const int32_t* src, const int32_t* dst, int64_t count, int64_t first,
                            int64_t step) {
     const int64_t pieces = (pool.page16 + kMove * kPiece - 1) / (kMove * kPiece);
@@ -166,7 +168,8 @@ __global__ __launch_bounds__(kPlan) void reserve_kernel(int32_t* __restrict__ ta
     }
 }
 
-// Plan of a fork: workspace before[n], from[n], to[n] (page to copy and its
+// Plan of a fork (64 new sequences, 1500 pages: 4.9 us, one workgroup's chain
+// of reads, prefix sums and stores): workspace before[n], from[n], to[n] (page to copy and its
 // place; to < 0: none).  Sets lens of the new sequences and counts of the new
 // pages; fork_apply fills the rows, counts the shared pages and copies.
 __global__ __launch_bounds__(kPlan) void fork_plan_kernel(const int32_t* __restrict__ tables, int64_t width,
@@ -225,6 +228,7 @@ __global__ __launch_bounds__(kPlan) void fork_plan_kernel(const int32_t* __restr
     }
 }
 
+// 64 sequences forked in 8 layers, 75.5 MB: 13 to 15 us, 5 to 5.8 TB/s.
 __global__ __launch_bounds__(kMove) void fork_apply_kernel(Pool pool, int32_t* __restrict__ tables, int64_t width,
                                                            const int32_t* __restrict__ lens, int32_t* __restrict__ refs,
                                                            int64_t seqs, int page_shift,
@@ -272,7 +276,8 @@ __global__ __launch_bounds__(kMove) void free_kernel(int32_t* __restrict__ table
     }
 }
 
-// Plan of a compaction: workspace count, from[half], to[half], place[pages]
+// Plan of a compaction (2049 pages: 8.8 us, three prefix sums over them, one
+// after the other): workspace count, from[half], to[half], place[pages]
 // (where each page goes).
 __global__ __launch_bounds__(kPlan) void compact_plan_kernel(const int32_t* refs, int64_t pages, int32_t* refs_out,
                                                              int32_t* __restrict__ live_out, int32_t* ws) {
