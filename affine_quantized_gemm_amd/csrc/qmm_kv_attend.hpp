@@ -728,9 +728,8 @@ __device__ __forceinline__ void join_parts(Shared sums, uint32_t at0, uint32_t s
 // of 64, up to 2k 11.6 us.  A call starts (lengths, plan, q, page ids, first
 // tokens) in 3 to 4 us and joins its parts in about 4; between them one row tile
 // is bound by its reads (6 TB/s over 131071 tokens), two by the vector ALUs:
-// 320 instructions a step of 32 tokens, of which a fifth makes operands of
-// codes, a fifth is the softmax, and the rest scales scores and P' (64 % busy
-// at 64 rows, the matrix cores 28 %).
+// 320 instructions a step of 32 tokens for operands out of codes, scaling the
+// scores, the softmax and P' (64 rows: 63 % busy, the matrix cores 28 %).
 template <int DT, int D, int GS, int RT, bool ROWS, bool NT_LOADS>
 __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT)) void attend_kernel(AttendParams a) {
     constexpr int kAttendWaves = attend_waves(RT, ROWS), kTiles = attend_tiles(RT, ROWS);
