@@ -418,6 +418,15 @@ __device__ __forceinline__ void keep_tokens(uint32_t& w01, uint32_t& w23, int n)
     w23 &= n >= 4 ? ~0u : n == 3 ? 0xFFFFu : 0u;
 }
 
+// Two halves, 0 for those that are infinite or NaN.
+template <int DT>
+__device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
+    constexpr uint32_t top = DT == DT_F16 ? 0x7C00u : 0x7F80u;
+    if ((w & top) == top) w &= 0xFFFF0000u;
+    if (((w >> 16) & top) == top) w &= 0xFFFFu;
+    return w;
+}
+
 // Issue priority of the wavefront.  The matrix products go first, so that a
 // SIMD's two wavefronts do not do their softmax at the same time; between
 // them the younger wavefront (`late`) goes first, which otherwise falls behind
@@ -442,17 +451,22 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
     const float4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
 
     // the largest scale of V, against 2^(E + 7): one or two pairs a lane
-    float big = 0.0f;
+    auto largest_scale = [&](bool finite) {
+        float big = 0.0f;
 #pragma unroll
-    for (int n = 0; n < (G == 8 ? 2 : 1); ++n) {
-        const int at = (lane + 64 * n) % (16 * G);  // (bundle, group), pair
-        uint32_t w = x[L::kVs + (at >> 1) * 4 + (at & 1)];
-        if constexpr (EDGE) {
-            const int tokens = left - (at >> 1) / G * 4 - 2 * (at & 1);
-            w &= tokens >= 2 ? ~0u : tokens == 1 ? 0xFFFFu : 0u;
+        for (int n = 0; n < (G == 8 ? 2 : 1); ++n) {
+            const int at = (lane + 64 * n) % (16 * G);  // (bundle, group), pair
+            uint32_t w = x[L::kVs + (at >> 1) * 4 + (at & 1)];
+            if constexpr (EDGE) {
+                const int tokens = left - (at >> 1) / G * 4 - 2 * (at & 1);
+                w &= tokens >= 2 ? ~0u : tokens == 1 ? 0xFFFFu : 0u;
+            }
+            if (finite) w = finite_halves<DT>(w);
+            big = fmaxf(big, fmaxf(half_f32<DT>(w, 0), half_f32<DT>(w, 1)));
         }
-        big = fmaxf(big, fmaxf(half_f32<DT>(w, 0), half_f32<DT>(w, 1)));
-    }
+        return big;
+    };
+    const float big = largest_scale(false);
 
     priority_products();
     // scores of all row tiles: sum_g b (sum of q) from the matrix core, + s (codes . q)
@@ -518,7 +532,7 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
     }
     if (__any(move)) {
         const float old_e = ref_e;
-        float all = big;
+        float all = largest_scale(true);  // (infinite ones leave the other groups' sums alone)
 #pragma unroll
         for (int n = 1; n < 16; n *= 2) all = fmaxf(all, __shfl_xor(all, n));
         all = max_j(all);
@@ -566,14 +580,20 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
     // sums of p b and p s, raw scales and biases as the operand: row i < 8 is
     // the bias of group i mod G, row 8 + i its scale.  (p is rounded, but
     // alike for both, so that the error is weighed by b + 7.5 s, the middle of the
-    // group's values.)
+    // group's values.)  Rows may not see a token whose values are infinite or
+    // NaN: its scale and bias are left out here, and the rows that do see it
+    // have them from P' (a bias is finite where the scale is).
     {
         Frag sb;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             uint32_t w[2];
             load_words<2>(x + L::kVs + ((4 * t + j) * G + i % G) * 4 + (i < 8 ? 2 : 0), w);
-            if constexpr (EDGE) keep_tokens(w[0], w[1], left - (16 * t + 4 * j));
+            if constexpr (EDGE) {
+                keep_tokens(w[0], w[1], left - (16 * t + 4 * j));
+                w[0] = finite_halves<DT>(w[0]);
+                w[1] = finite_halves<DT>(w[1]);
+            }
             sb.v[2 * t] = w[0];
             sb.v[2 * t + 1] = w[1];
         }
@@ -601,8 +621,14 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
             for (int r = 0; r < 4; ++r) s[r] = half_f32<DT>(w[r / 2], r & 1);
 #pragma unroll
             for (int u = 0; u < RT; ++u) {
-                pp[u].v[2 * t] = pack_f16(sc[u][t][0] * s[0], sc[u][t][1] * s[1]);
-                pp[u].v[2 * t + 1] = pack_f16(sc[u][t][2] * s[2], sc[u][t][3] * s[3]);
+                float ps[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    ps[r] = sc[u][t][r] * s[r];
+                    if constexpr (EDGE) ps[r] = see[u][t][r] ? ps[r] : 0.0f;  // (s may be infinite)
+                }
+                pp[u].v[2 * t] = pack_f16(ps[0], ps[1]);
+                pp[u].v[2 * t + 1] = pack_f16(ps[2], ps[3]);
             }
         }
 #pragma unroll

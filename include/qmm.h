@@ -419,6 +419,8 @@ int qmm_kv_read(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_
  *     new tokens j whose bit j is set in the row's word (a draft tree: the
  *     row's own token and its ancestors).
  *   - A row that sees nothing gives zeros and lse = -infinity.
+ *   - What a row does not see has no part in it, infinite or NaN as it may be;
+ *     infinite or NaN values that it sees reach their group of the output.
  * fp32 accumulation, softmax and sums; k_hat and v_hat are not rounded; for
  * the second product the probabilities times the scale of their value are
  * rounded to fp16 (11 bits, either dt), for the biases to dt; one rounding to

@@ -319,6 +319,40 @@ def test_attend_masks(Q):
         check_attend(Q, c, tables, lens, new, 4, 101, mask=mask)
 
 
+@pytest.mark.parametrize("dt,gs", [("f16", 32), ("bf16", 64), ("f16", 128)])
+@pytest.mark.parametrize("heads", [2, 40])
+def test_attend_infinite_values(Q, dt, gs, heads):
+    """Draft tokens of infinite and NaN values: the rows that do not see them are as if they were not; a value that all
+    rows see takes its own group only."""
+    print(f"attend infinite {dt} gs={gs} heads={heads}", flush=True)
+    inf, nan = float("inf"), float("nan")
+    masks = torch.tensor([0b1, 0b11, 0b101, 0b1000, 0b10001, 0b100001], dtype=torch.int64, device="cuda")
+    k, v = (values(300, 1, 128, dt, 150 + i) for i in (0, 1))
+    q = synth.normal((6, heads, 128), 1.0, dt, 152).cuda()
+    tables, lens = i32(np.arange(5)[None]), i32([300])
+    out = []
+    for bad in (False, True):
+        cache = Q.KVCache.empty(1, 5, 1, 128, gs, 64, DT[dt])
+        if bad:  # the fourth and sixth new tokens
+            k[297], v[297], k[299], v[299, 0, :gs] = nan, inf, inf, -inf
+        cache.append(0, k.cuda(), v.cuda(), tables, lens)
+        out.append(cache.attend(0, q, tables, lens, mask=masks, lse=True))
+    (a, la), (b, lb) = out
+    others = [0, 1, 2, 4]
+    assert torch.isfinite(a).all()
+    assert torch.equal(a[others].view(torch.int16), b[others].view(torch.int16)) and torch.equal(la[others], lb[others])
+    assert not torch.isfinite(b[3]).any() and not torch.isfinite(b[5, :, :gs]).any()
+    # before the new tokens, where every row sees it: one group of one token
+    if gs < 128:
+        v[297], k[297], k[299], v[299], v[20, 0, gs:2 * gs] = 0, 0, 0, 0, inf
+        cache.append(0, k.cuda(), v.cuda(), tables, lens)
+        c = cache.attend(0, q, tables, lens, mask=masks)
+        seen = torch.ones(128, dtype=torch.bool)
+        seen[gs:2 * gs] = False
+        assert not torch.isfinite(c[..., ~seen]).any()
+        assert torch.equal(c[others][..., seen].view(torch.int16), a[others][..., seen].view(torch.int16))
+
+
 def test_attend_nothing_to_see(Q):
     """No tokens, lengths below the new rows, no page, a table of width 0."""
     lens, new = np.array([0, 0, 2, 40, -5]), np.array([1, 3, 5, 2, 2])
