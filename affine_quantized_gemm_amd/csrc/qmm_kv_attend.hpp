@@ -451,22 +451,18 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
     const float4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
 
     // the largest scale of V, against 2^(E + 7): one or two pairs a lane
-    auto largest_scale = [&](bool finite) {
-        float big = 0.0f;
+    uint32_t scales[G == 8 ? 2 : 1];
+    float big = 0.0f;
 #pragma unroll
-        for (int n = 0; n < (G == 8 ? 2 : 1); ++n) {
-            const int at = (lane + 64 * n) % (16 * G);  // (bundle, group), pair
-            uint32_t w = x[L::kVs + (at >> 1) * 4 + (at & 1)];
-            if constexpr (EDGE) {
-                const int tokens = left - (at >> 1) / G * 4 - 2 * (at & 1);
-                w &= tokens >= 2 ? ~0u : tokens == 1 ? 0xFFFFu : 0u;
-            }
-            if (finite) w = finite_halves<DT>(w);
-            big = fmaxf(big, fmaxf(half_f32<DT>(w, 0), half_f32<DT>(w, 1)));
+    for (int n = 0; n < (G == 8 ? 2 : 1); ++n) {
+        const int at = (lane + 64 * n) % (16 * G);  // (bundle, group), pair
+        scales[n] = x[L::kVs + (at >> 1) * 4 + (at & 1)];
+        if constexpr (EDGE) {
+            const int tokens = left - (at >> 1) / G * 4 - 2 * (at & 1);
+            scales[n] &= tokens >= 2 ? ~0u : tokens == 1 ? 0xFFFFu : 0u;
         }
-        return big;
-    };
-    const float big = largest_scale(false);
+        big = fmaxf(big, fmaxf(half_f32<DT>(scales[n], 0), half_f32<DT>(scales[n], 1)));
+    }
 
     priority_products();
     // scores of all row tiles: sum_g b (sum of q) from the matrix core, + s (codes . q)
@@ -532,7 +528,12 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
     }
     if (__any(move)) {
         const float old_e = ref_e;
-        float all = largest_scale(true);  // (infinite ones leave the other groups' sums alone)
+        float all = 0.0f;  // (infinite scales leave the other groups' sums alone)
+#pragma unroll
+        for (int n = 0; n < (G == 8 ? 2 : 1); ++n) {
+            const uint32_t w = finite_halves<DT>(scales[n]);
+            all = fmaxf(all, fmaxf(half_f32<DT>(w, 0), half_f32<DT>(w, 1)));
+        }
 #pragma unroll
         for (int n = 1; n < 16; n *= 2) all = fmaxf(all, __shfl_xor(all, n));
         all = max_j(all);
@@ -747,11 +748,11 @@ __device__ __forceinline__ void join_parts(Shared sums, uint32_t at0, uint32_t s
 // group blockIdx.y (row = new token * group + head within the group).
 //
 // Measured (bf16 or fp16, 32 heads, 8 kv heads of 128, groups of 64 unless
-// said): one token over 777 tokens 9.5 us, 32 sequences of 1k..4k 24.4 us
+// said): one token over 777 tokens 9.6 us, 32 sequences of 1k..4k 24.4 us
 // (3.9 TB/s; 13.7 us of reading), 16 sequences of 4..6 rows over 8k 39.6 us
 // (3.8 TB/s; 21.6), one token over 131071 30.2 us (4.7 TB/s; 20.6), 64 rows of
 // 4 sequences over 16k 116 us (565 TFLOP/s; 54); 8 trees of 13 rows, 16 heads
-// of 64, up to 2k 11.6 us.  A call starts (lengths, plan, q, page ids, first
+// of 64, up to 2k 11.8 us.  A call starts (lengths, plan, q, page ids, first
 // tokens) in 3 to 4 us and joins its parts in about 4; between them one row tile
 // is bound by its reads (6 TB/s over 131071 tokens), two by the vector ALUs:
 // 320 instructions a step of 32 tokens for operands out of codes, scaling the
