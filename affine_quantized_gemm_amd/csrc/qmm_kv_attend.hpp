@@ -25,12 +25,14 @@
 // P' is lost from every even code's product, downwards.  So what these sums
 // are centred by is summed in the same form, over the codes 8..15, and loses
 // as much.  (Without, the average of 16k tokens is 1e-4 of itself off, half of
-// fp16's rounding.)  Unpacking a word of 8 codes takes four ands and a
-// shift, no conversion and no offset to take away again.  The factors 2^24
-// go into the scores' scale and the last step; the 16 of the odd codes into
-// the d order of Q (q / 16) and into the last step.  Q is scaled per row by a
-// power of two into fp16's range, for bf16 too, so there is one form for
-// both types.
+// fp16's rounding.)  The scores' sums lose what depends on the row's q alone,
+// found with the codes 8..15 again once for a row and given back with the biases
+// (the logarithms of the sums were 1e-6 of themselves off, now 1e-7 to 7e-7).
+// Unpacking a word of 8 codes takes four ands and a shift, no conversion and
+// no offset to take away again.  The factors 2^24 go into the scores' scale and
+// the last step; the 16 of the odd codes into the d order of Q (q / 16) and
+// into the last step.  Q is scaled per row by a power of two into fp16's
+// range, for bf16 too, so there is one form for both types.
 //
 // Layout of v_mfma_f32_16x16x32_f16: lane l = 16 j + i supplies A[i][8 j + e]
 // and B[8 j + e][i], e = 0..7, and receives D[4 j + r][i], r = 0..3.
@@ -334,7 +336,7 @@ template <int D, int GS>
 struct RowTile {
     static constexpr int S = D / 32, G = D / GS, NT = D / 16;
     Frag q[S];        // Q^T operand
-    Frag qs;          // sums of the groups' q, times kQsUnit, in three pieces: slot 8 j + g, piece j
+    Frag qs;          // sums of the groups' q, times kQsUnit, in three pieces: slot 8 j + g, piece j; 24 + g: what is lost
     float cs;         // score -> log2 units
     float m, l;       // M; this lane's share of the sum of p
     float4_t zb;      // sums p b (rows 0..7: group) and p s (rows 8..15)
@@ -368,7 +370,7 @@ __device__ __forceinline__ uint32_t pack_dt(float lo, float hi) {
 
 // Row tile's Q from its words w: values of row i, d = 32 s + 8 j + e.
 template <int DT, int D, int GS>
-__device__ __forceinline__ void make_q(RowTile<D, GS>& t, const uint32_t (&w)[D / 32][4], float scale, int j) {
+__device__ __forceinline__ void make_q(RowTile<D, GS>& t, const uint32_t (&w)[D / 32][4], float scale, int i, int j) {
     constexpr int S = D / 32, G = D / GS;
     float f[S][8];
     float top = 0.0f;
@@ -399,13 +401,19 @@ __device__ __forceinline__ void make_q(RowTile<D, GS>& t, const uint32_t (&w)[D 
     t.qs.v[0] = t.qs.v[1] = t.qs.v[2] = t.qs.v[3] = 0;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-        const float x = sum_j(sums[g]) * (up[0] * kQsUnit<DT>);
+        const float sum = sum_j(sums[g]) * up[0], x = sum * kQsUnit<DT>;
         // three pieces of 11 or 8 bits, exact up to 2^-24 of x (fp16: 2^-25, 2^-31 of the row's largest q)
         const uint32_t h0 = bits_of<DT>(x);
         const float r1 = x - DtOps<DT>::to_f32(static_cast<uint16_t>(h0));
         const uint32_t h1 = bits_of<DT>(r1);
         const uint32_t h2 = bits_of<DT>(r1 - DtOps<DT>::to_f32(static_cast<uint16_t>(h1)));
-        const uint32_t h = j == 0 ? h0 : j == 1 ? h1 : j == 2 ? h2 : 0u;
+        // what the codes' products with this q lose to the cut (rows of codes 8..15, against 11.5 times the sum)
+        const Frag codes = codes8(0x11111111u * (8 + i % 8));
+        float4_t cut = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = g * (GS / 32); s < (g + 1) * (GS / 32); ++s) cut = mf::mfma<DT_F16>(codes, t.q[s], cut);
+        const float lost = 0x1p-24f * 11.5f * sum - 0.0625f * sum_j(cut[0] + cut[1] + cut[2] + cut[3]);
+        const uint32_t h = j == 0 ? h0 : j == 1 ? h1 : j == 2 ? h2 : bits_of<DT>(lost * (0x1p24f * kQsUnit<DT>));
         t.qs.v[g / 2] |= h << (16 * (g & 1));
     }
     // log2(e) * |scale| * 2^24 / 2^k
@@ -465,7 +473,7 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
     }
 
     priority_products();
-    // scores of all row tiles: sum_g b (sum of q) from the matrix core, + s (codes . q)
+    // scores of all row tiles: sum_g b (sum of q) and s (what the codes' products lose) from the matrix core, + s (codes . q)
     float sc[RT][2][4];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -473,7 +481,7 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
         load_words<S>(x + t * (L::kCodes / 2) + (4 * i + j) * S, k);
         Frag kb;
         kb.v[0] = kb.v[1] = kb.v[2] = kb.v[3] = 0;
-        const uint16_t* hb = reinterpret_cast<const uint16_t*>(x + L::kKs) + ((4 * t + i / 4) * G) * 8 + 4 + i % 4;
+        const uint16_t* hb = reinterpret_cast<const uint16_t*>(x + L::kKs) + ((4 * t + i / 4) * G) * 8 + (j < 3 ? 4 : 0) + i % 4;
 #pragma unroll
         for (int g = 0; g < G; ++g) kb.v[g / 2] |= static_cast<uint32_t>(hb[8 * g]) << (16 * (g & 1));
         float4_t acc[RT], p[RT][G];
@@ -748,10 +756,11 @@ __device__ __forceinline__ void join_parts(Shared sums, uint32_t at0, uint32_t s
 // group blockIdx.y (row = new token * group + head within the group).
 //
 // Measured (bf16 or fp16, 32 heads, 8 kv heads of 128, groups of 64 unless
-// said): one token over 777 tokens 9.6 us, 32 sequences of 1k..4k 24.4 us
-// (3.9 TB/s; 13.7 us of reading), 16 sequences of 4..6 rows over 8k 39.6 us
-// (3.8 TB/s; 21.6), one token over 131071 30.2 us (4.7 TB/s; 20.6), 64 rows of
-// 4 sequences over 16k 116 us (565 TFLOP/s; 54); 8 trees of 13 rows, 16 heads
+// said): one token over 777 tokens 9.9 us, 32 sequences of 1k..4k 24.9 us
+// (3.8 TB/s; 13.7 us of reading), 16 sequences of 4..6 rows over 8k 40.3 us
+// (3.7 TB/s; 21.6), one token over 131071 30.5 us (4.7 TB/s; 20.6), 64 rows of
+// 4 sequences over 16k 120 us (546 TFLOP/s; 54; 111 in
+// a row of calls); 8 trees of 13 rows, 16 heads
 // of 64, up to 2k 11.8 us.  A call starts (lengths, plan, q, page ids, first
 // tokens) in 3 to 4 us and joins its parts in about 4; between them one row tile
 // is bound by its reads (6 TB/s over 131071 tokens), two by the vector ALUs:
@@ -848,7 +857,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
     RowTile<D, GS> rows[RT];
 #pragma unroll
     for (int u = 0; u < RT; ++u) {
-        make_q<DT, D, GS>(rows[u], qw[u], a.scale, j);
+        make_q<DT, D, GS>(rows[u], qw[u], a.scale, i, j);
         rows[u].bits = bits[u];
         rows[u].m = kFar;
         rows[u].l = 0.0f;
