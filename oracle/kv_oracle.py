@@ -106,9 +106,12 @@ def read(c, layer, tables, lens, starts, kv_heads):
 
 
 def attend(c, layer, q, tables, lens, starts, scale, mask=None):
-    """q [rows, heads, dim] fp64 -> out, lse, and per element how far a kernel may be off.
+    """q [rows, heads, dim] fp64 -> out, lse, and per element a coarse bound of how far a kernel may be off.
 
-    The bound (u: half a unit in the last place of the type, relative):
+    The bound is that of a plainer kernel, which rounds more, and over many
+    tokens it is as large as the output (``attend_bound`` follows the
+    roundings that there are).  u: half a unit in the last place of the type,
+    relative:
       * out is rounded once: u |out|;
       * p s is rounded to the type before the second product, whose codes are
         taken about their middle (|code - 8| <= 8): 8 u sum p s, twice that
@@ -160,6 +163,83 @@ def attend(c, layer, q, tables, lens, starts, scale, mask=None):
                     tol[row + i, x] = u * np.abs(o) + (16 * u * ps.sum(0) + small) / total + rel * size + 2.0 ** -25
                     lse[row + i, x] = top + np.log(total)
                     ltol[row + i, x] = 2 * e + 2.0 ** -20 * (1 + abs(top) + len(p) / 4096)
+        row += n
+    return out, lse, tol, ltol
+
+
+def attend_bound(c, layer, q, tables, lens, starts, scale, mask=None):
+    """As ``attend``, with a bound that follows the kernel rounding by rounding: out, lse, tol, ltol.
+
+    With weights w_t = p_t / l of the tokens that a row sees, p <= 1, out = sum w (s (code - 7.5) + m), m = b + 7.5 s.
+    N: tokens of the sequence.  u: 2^-11 (fp16) or 2^-8 (bf16), a rounding to the type.
+
+      * out is rounded once, after all that follows: half a unit in its last place (fp16: at least 2^-25);
+      * p s is an fp16 operand, for either type: 2^-11 |code - 7.5| w s;  the largest p s of a row and group counts
+        for at least 2^-4, so one below 2^-10 of it (a subnormal) is off by up to 2^-21 of that largest instead;
+      * the matrix core cuts each product with a code off at 2^-18 of a code times the largest p s of the 32 of one
+        product, in the sum and in what centres it: 2 * 32 * 2^-18 w s;
+      * p is rounded to the type for the middles m, and so is the sum that they are divided by: only what m differs
+        from its mean counts, 2 u w |m - mean| (a mean per part of the sequence, hence 2);  fp16: the row's largest p
+        counts for at least 4, one below 2^-16 of it is off by up to 2^-27 of that;
+      * the score of a token is off by E = |scale| (2 * 32 * 2^-18 sum_g s_g sum_(32 d in g) max |q| [the same cut]
+        + 2^-21 sum_g (15 s_g + |b_g|) sum_(d in g) |q_d|) + 2^-21 (|score| + |top| + 8), the last for the argument and the
+        value of the exponential: w E |v - out|;
+      * fp32 sums: of n = N / 32 + 4 steps, 2^-22 n of the 30 w s that the codes and their centre add up to and of
+        w (|b| + 7.5 s), and the N / 4 of l, 2^-24 each, of out.
+    """
+    rows, heads, dim = q.shape
+    hk, gs = c["pool"].shape[2], c["gs"]
+    G = dim // gs
+    half = c["dt"] == "f16"
+    u = 2.0 ** -11 if half else 2.0 ** -8
+    out, lse = np.zeros((rows, heads, dim)), np.full((rows, heads), -np.inf)
+    tol, ltol = np.zeros_like(out), np.zeros_like(lse)
+    cap = tables.shape[1] * c["page"]
+    row = 0
+    for b in range(len(lens)):
+        n = int(starts[b + 1] - starts[b])
+        length = min(max(int(lens[b]), 0), cap)
+        pages = [page_of(c, tables, b, t) for t in range(length)]
+        got = [t for t in range(length) if pages[t] >= 0]
+        new = np.array(got, dtype=np.int64) - (int(lens[b]) - n)
+        for h in range(hk if n else 0):
+            data = [[load(c, layer, pages[t], h, t % c["page"], part) for t in got] for part in (0, 1)]
+            kc, ks, kb, vc, vs, vb = (np.array([d[j] for d in data[i]]).reshape(len(got), dim)
+                                      for i in (0, 1) for j in (0, 1, 2))
+            kk, vv = ks * kc + kb, vs * vc + vb
+            for i in range(n):
+                word = int(mask[row + i]) if mask is not None else (2 << i) - 1
+                see = np.array([j < 0 or (j < 64 and word >> int(j) & 1) for j in new], dtype=bool)
+                if not see.any():
+                    continue
+                s, v, m, off = vs[see], vv[see], vb[see] + 7.5 * vs[see], np.abs(vc[see] - 7.5)
+                for x in range(h * (heads // hk), (h + 1) * (heads // hk)):
+                    qq = q[row + i, x]
+                    a = np.abs(qq)
+                    sc = scale * (kk[see] @ qq)
+                    top = sc.max()
+                    p = np.exp(sc - top)
+                    total = p.sum()
+                    w = (p / total)[:, None]
+                    o = (w * v).sum(0)
+                    chunks = a.reshape(dim // 32, 32).max(1).repeat(32) / 32
+                    e = abs(scale) * (2.0 ** -12 * (ks[see] @ chunks) + 2.0 ** -21 * ((15 * ks[see] + np.abs(kb[see])) @ a))
+                    e = (e + 2.0 ** -21 * (np.abs(sc) + abs(top) + 8))[:, None]
+                    steps, ws, ps = length / 32 + 4, w * s, p[:, None] * s
+                    mean = (w * m).sum(0)
+                    t = 2.0 ** -11 * (ws * off).sum(0)
+                    t += 2.0 ** -21 * ps.max(0) / total * (off * (ps < 2.0 ** -9 * ps.max(0))).sum(0)
+                    t += 2.0 ** -12 * ws.sum(0)
+                    t += 2 * u * (w * np.abs(m - mean)).sum(0)
+                    if half:
+                        t += 2.0 ** -27 / total * (np.abs(m - mean) * (p < 2.0 ** -15)[:, None]).sum(0)
+                    t += 1.01 * (w * e * np.abs(v - o)).sum(0)
+                    t += 2.0 ** -22 * steps * (30 * ws + w * (np.abs(vb[see]) + 7.5 * s)).sum(0)
+                    t += 2.0 ** -24 * (length / 4 + 64) * np.abs(o)
+                    t += np.maximum(u * 2.0 ** (np.frexp(np.abs(o) + t)[1] - 1), 2.0 ** -25 if half else 0.0)
+                    out[row + i, x], tol[row + i, x] = o, t
+                    lse[row + i, x] = top + np.log(total)
+                    ltol[row + i, x] = 1.01 * (w * e).sum() + 2.0 ** -20 * (1 + abs(top)) + 2.0 ** -24 * length / 4
         row += n
     return out, lse, tol, ltol
 

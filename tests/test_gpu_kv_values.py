@@ -1,0 +1,145 @@
+"""Attention over the paged K/V cache within the bound that follows its roundings (``kv_oracle.attend_bound``), on
+ordinary values and on those where a running reference or a small type goes wrong."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import synth
+from oracle import kv_oracle as KO
+from oracle import qmm_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f16": torch.float16, "bf16": torch.bfloat16}
+FORMATS = [(dim, gs) for dim in (64, 128, 256) for gs in (32, 64, 128) if gs <= dim]
+BOTH = pytest.mark.parametrize("dt", ["f16", "bf16"])
+
+
+@pytest.fixture(scope="module")
+def Q():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import affine_quantized_gemm_amd as Q
+    return Q
+
+
+def i32(a):
+    return torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")
+
+
+def normal(shape, dt, seed, std=1.0):
+    return synth.normal(shape, std, dt, seed)
+
+
+def cache_of(k, v, gs, dt, lens, page=64, seed=1):
+    """A cache that holds the sequences' k and v [tokens, kv_heads, dim], and its tables; poison elsewhere."""
+    lens = np.asarray(lens)
+    need = -(-lens // page)
+    pages = int(need.sum()) + 1
+    c = KO.new_cache(1, pages, k.shape[1], k.shape[2], gs, page, dt, fill=0x7FFF7FFF)
+    order, at = np.random.default_rng(seed).permutation(pages), 0
+    tables = np.full((len(lens), int(need.max()) + 1), -1, np.int32)
+    for b, n in enumerate(need):
+        tables[b, :n] = order[at:at + n]
+        at += n
+    KO.append(c, 0, synth.to_oracle(k), synth.to_oracle(v), tables, lens, np.concatenate([[0], np.cumsum(lens)]))
+    return c, tables
+
+
+def call(Q, c, q, tables, lens, new, mask=None, scale=None, max_len=None):
+    """(out, lse) of the kernel."""
+    cache = Q.KVCache(torch.from_numpy(c["pool"].view(np.int32).copy()).cuda(), c["dim"], c["gs"], c["page"], DT[c["dt"]])
+    kw = {"starts": i32(np.concatenate([[0], np.cumsum(new)])), "max_new": int(max(new))} if len(set(new)) > 1 else {}
+    m = None if mask is None else torch.tensor(mask, dtype=torch.int64, device="cuda")
+    return cache.attend(0, q.cuda(), i32(tables), i32(lens), mask=m, scale=scale, max_len=max_len, lse=True, **kw)
+
+
+def check(Q, c, q, tables, lens, new, mask=None, scale=None, max_len=None, oracle=None):
+    """The kernel against the oracle, within its bound; returns the kernel's and the oracle's results."""
+    dt = c["dt"]
+    scale = 1 / math.sqrt(c["dim"]) if scale is None else scale
+    if oracle is None:
+        oracle = KO.attend_bound(c, 0, O.to_f64(synth.to_oracle(q), dt), tables, lens,
+                                 np.concatenate([[0], np.cumsum(new)]), scale, mask)
+    out, lse, tol, ltol = oracle
+    got, glse = call(Q, c, q, tables, lens, new, mask, scale, max_len)
+    g, gl = O.to_f64(synth.to_oracle(got), dt), glse.cpu().numpy().astype(np.float64)
+    seen = ~np.isneginf(lse)
+    bad = ~(np.abs(g - out) <= tol)
+    with np.errstate(invalid="ignore"):
+        print(f"  err/bound {np.nanmax(np.abs(g - out) / np.maximum(tol, 1e-300)):.3f}, "
+              f"lse {np.nanmax(np.abs(gl - lse)[seen] / ltol[seen], initial=0):.3f}, "
+              f"not finite {np.count_nonzero(~np.isfinite(g))}", flush=True)
+    assert not bad.any(), f"{np.count_nonzero(bad)} of {bad.size} beyond the bound"
+    assert np.array_equal(np.isneginf(gl), ~seen) and (g[~seen] == 0).all()
+    assert (np.abs(gl - lse)[seen] <= ltol[seen]).all()
+    return got, oracle
+
+
+def offset_keys(n, kv_heads, dim, dt, seed):
+    """Keys as a model leaves them: channels with offsets."""
+    return (normal((n, kv_heads, dim), dt, seed).float() + normal((1, kv_heads, dim), "f16", seed + 1, 1.5).float()).to(DT[dt])
+
+
+# ---- the bound, at ordinary values ----
+
+@BOTH
+@pytest.mark.parametrize("dim,gs", FORMATS)
+def test_formats(Q, dt, dim, gs):
+    print(f"formats {dt} D={dim} gs={gs}", flush=True)
+    lens, new = np.array([1, 33, 70, 130]), np.array([1, 4, 6, 2])
+    n = int(lens.sum())
+    c, tables = cache_of(offset_keys(n, 2, dim, dt, 10), normal((n, 2, dim), dt, 12), gs, dt, lens, page=32)
+    check(Q, c, normal((13, 6, dim), dt, 13), tables, lens, new)
+
+
+@BOTH
+@pytest.mark.parametrize("rows,heads", [(1, 2), (5, 2), (5, 8), (40, 1)])
+def test_long(Q, dt, rows, heads):
+    """Cut over workgroups and not, one tile of rows and more."""
+    print(f"long {dt} rows={rows} heads={heads}", flush=True)
+    lens, new = np.array([1700, 600 + rows]), np.full(2, rows)
+    n = int(lens.sum())
+    c, tables = cache_of(offset_keys(n, 1, 128, dt, 20), normal((n, 1, 128), dt, 22), 64, dt, lens)
+    q = normal((2 * rows, heads, 128), dt, 23)
+    _, oracle = check(Q, c, q, tables, lens, new)
+    check(Q, c, q, tables, lens, new, max_len=64, oracle=oracle)
+
+
+@BOTH
+def test_by_rows(Q, dt):
+    """Enough short sequences for workgroups by rows."""
+    print(f"by rows {dt}", flush=True)
+    lens = np.array([40 + b % 9 for b in range(40)])
+    n = int(lens.sum())
+    c, tables = cache_of(offset_keys(n, 4, 64, dt, 30), normal((n, 4, 64), dt, 32), 32, dt, lens)
+    check(Q, c, normal((40 * 18, 8, 64), dt, 33), tables, lens, np.full(40, 18), max_len=48)
+
+
+@BOTH
+@pytest.mark.parametrize("scores", ["flat", "rising", "falling"])
+@pytest.mark.parametrize("sizes", ["rising", "falling"])
+def test_ramps(Q, dt, scores, sizes):
+    """Scores and values' sizes that rise or fall along a sequence by many times what a reference lets through."""
+    print(f"ramps {dt} scores {scores} sizes {sizes}", flush=True)
+    n, dim = 700, 64
+    at = torch.linspace(0, 1, n)[:, None, None]
+    k = normal((n, 1, dim), dt, 90, 0.2).float()
+    k = k + {"flat": 0 * at, "rising": 5 * at, "falling": 5 - 5 * at}[scores]
+    e = 14 * at - 7 if dt == "f16" else 60 * at - 30
+    v = normal((n, 1, dim), dt, 92).float() * 2.0 ** (e if sizes == "rising" else -e)
+    q = (normal((1, 5, dim), dt, 93).float() * 0.2 + 1.0).to(DT[dt])
+    c, tables = cache_of(k.to(DT[dt]), v.to(DT[dt]), 32, dt, [n])
+    check(Q, c, q, tables, np.array([n]), np.array([1]), scale=0.5)
+
+
+@pytest.mark.parametrize("dt,size", [("f16", 2.0 ** -14), ("f16", 2.0 ** -9), ("f16", 300.0), ("f16", 1e4),
+                                     ("bf16", 2.0 ** -60), ("bf16", 2.0 ** 60)])
+def test_sizes(Q, dt, size):
+    print(f"size {dt} {size}", flush=True)
+    k, v = normal((400, 1, 128), dt, 100), (normal((400, 1, 128), dt, 102).float() * size).to(DT[dt])
+    c, tables = cache_of(k, v, 64, dt, [400])
+    check(Q, c, normal((1, 20, 128), dt, 103), tables, np.array([400]), np.array([1]))
