@@ -143,3 +143,53 @@ def test_sizes(Q, dt, size):
     k, v = normal((400, 1, 128), dt, 100), (normal((400, 1, 128), dt, 102).float() * size).to(DT[dt])
     c, tables = cache_of(k, v, 64, dt, [400])
     check(Q, c, normal((1, 20, 128), dt, 103), tables, np.array([400]), np.array([1]))
+
+
+# ---- graphs ----
+
+@BOTH
+def test_graph_of_a_step_over_real_values(Q, dt):
+    """append + attend captured once, replayed as the lengths grow, every position that is seen written before:
+    finite, bit for bit the eager calls, and within the oracle's bound."""
+    print(f"graph {dt}", flush=True)
+    dim, gs, page, kv_heads, heads, n0 = 128, 64, 32, 2, 8, [1170, 45]
+    k, v = offset_keys(sum(n0), kv_heads, dim, dt, 140), normal((sum(n0), kv_heads, dim), dt, 142)
+    c = KO.new_cache(1, 48, kv_heads, dim, gs, page, dt, fill=0x7FFF7FFF)
+    tables = np.full((2, 40), -1, np.int32)
+    tables[0], tables[1, :8] = np.random.default_rng(4).permutation(40), np.arange(40, 48)
+    KO.append(c, 0, synth.to_oracle(k), synth.to_oracle(v), tables, n0, [0, n0[0], sum(n0)])
+    make = lambda: Q.KVCache(torch.from_numpy(c["pool"].view(np.int32).copy()).cuda(), dim, gs, page, DT[dt])
+    captured, eager = make(), make()
+    t, lens = i32(tables), i32([n + 1 for n in n0])
+    q, kn, vn = (torch.zeros(2, h, dim, dtype=DT[dt], device="cuda") for h in (heads, kv_heads, kv_heads))
+    out, lse = torch.zeros_like(q), torch.zeros(2, heads, device="cuda")
+    ws = captured.attend_workspace(2, 1, 2, heads, 1280)
+    step = lambda: (captured.append(0, kn, vn, t, lens),
+                    captured.attend(0, q, t, lens, out=out, lse=lse, max_len=1280, workspace=ws))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for r in range(12):
+        new = np.array([n + 1 + r for n in n0])
+        data = [normal(tuple(x.shape), dt, 150 + 3 * r + i) for i, x in enumerate((q, kn, vn))]
+        for x, d in zip((q, kn, vn), data):
+            x.copy_(d)
+        lens.copy_(i32(new))
+        g.replay()
+        eager.append(0, kn, vn, t, lens)
+        want, wlse = eager.attend(0, q, t, lens, lse=True, max_len=1280)
+        torch.cuda.synchronize()
+        assert torch.equal(captured.pool, eager.pool)
+        assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16)) and torch.equal(lse, wlse), r
+        KO.append(c, 0, synth.to_oracle(data[1]), synth.to_oracle(data[2]), tables, new, [0, 1, 2])
+        if r % 5 == 0:
+            o, ls, tol, ltol = KO.attend_bound(c, 0, O.to_f64(synth.to_oracle(data[0]), dt), tables, new, [0, 1, 2],
+                                               dim ** -0.5)
+            assert (np.abs(O.to_f64(synth.to_oracle(out), dt) - o) <= tol).all()
+            assert (np.abs(lse.cpu().numpy() - ls) <= ltol).all()
