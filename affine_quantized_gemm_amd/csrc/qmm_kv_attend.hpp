@@ -339,7 +339,8 @@ struct RowTile {
     Frag qs;          // sums of the groups' q, times kQsUnit, in three pieces: slot 8 j + g, piece j; 24 + g: what is lost
     float cs;         // score -> log2 units
     float m, l;       // M; this lane's share of the sum of p
-    float4_t zb;      // sums p b (rows 0..7: group) and p s (rows 8..15)
+    float4_t zb;      // sums p b (rows 0..7: group; 7: of p alone, where there are fewer) and p s (rows 8..15)
+    float4_t zp;      // 8 groups: sums of p as zb has it, every row alike
     float4_t z[G];    // lanes j = 0, 1: sum P'; 2, 3: 4 j + r times it, as a code
     float4_t o[NT];
     uint64_t bits;    // new tokens that the row sees
@@ -350,6 +351,10 @@ struct RowTile {
 // scaled to 2^15), so they are brought to 2^-9 and their product scaled.
 template <int DT>
 constexpr float kQsUnit = DT == DT_F16 ? 0x1p-9f : 0x1p-24f;
+
+// 1 as DT, twice.
+template <int DT>
+constexpr uint32_t kOnes = DT == DT_F16 ? 0x3C003C00u : 0x3F803F80u;
 
 // One value as DT's bits, nearest.
 template <int DT>
@@ -558,6 +563,9 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
             rows[u].l *= f;
 #pragma unroll
             for (int r = 0; r < 4; ++r) rows[u].zb[r] *= f;
+            if constexpr (G == 8)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) rows[u].zp[r] *= f;
 #pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -587,9 +595,11 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
         }
     }
     // sums of p b and p s, raw scales and biases as the operand: row i < 8 is
-    // the bias of group i mod G, row 8 + i its scale.  (p is rounded, but
-    // alike for both, so that the error is weighed by b + 7.5 s, the middle of the
-    // group's values.)  Rows may not see a token whose values are infinite or
+    // the bias of group i mod G, row 8 + i its scale.  p is rounded to the type
+    // here (8 bits for bf16), so the sum of the same rounded p is kept beside
+    // them (row 7, a group's double where G < 8): the mean of the middles
+    // b + 7.5 s is theirs over that, and the rounding is weighed by what they
+    // differ by, not by what they are.  Rows may not see a token whose values are infinite or
     // NaN: its scale and bias are left out here, and the rows that do see it
     // have them from P' (a bias is finite where the scale is).
     {
@@ -603,11 +613,17 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
                 w[0] = finite_halves<DT>(w[0]);
                 w[1] = finite_halves<DT>(w[1]);
             }
-            sb.v[2 * t] = w[0];
-            sb.v[2 * t + 1] = w[1];
+            sb.v[2 * t] = G < 8 && i == 7 ? kOnes<DT> : w[0];
+            sb.v[2 * t + 1] = G < 8 && i == 7 ? kOnes<DT> : w[1];
         }
 #pragma unroll
         for (int u = 0; u < RT; ++u) rows[u].zb = mf::mfma<DT>(sb, p16[u], rows[u].zb);
+        if constexpr (G == 8) {
+            Frag one;
+            one.v[0] = one.v[1] = one.v[2] = one.v[3] = kOnes<DT>;
+#pragma unroll
+            for (int u = 0; u < RT; ++u) rows[u].zp = mf::mfma<DT>(one, p16[u], rows[u].zp);
+        }
     }
     priority_products();
     // P' and the second product: tile n = 4 c + q of 16 d, from nibble q of the words of quad c
@@ -861,7 +877,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
         rows[u].bits = bits[u];
         rows[u].m = kFar;
         rows[u].l = 0.0f;
-        rows[u].zb = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        rows[u].zb = rows[u].zp = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int g = 0; g < G; ++g) rows[u].z[g] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -902,10 +918,13 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
 #pragma unroll
     for (int u = 0; u < RT; ++u) {
         rows[u].l = sum_j(rows[u].l);
+        // l over the sum of the rounded p (row 7 of zb: lanes j = 1)
+        const float rounded = G == 8 ? rows[u].zp[0] : __shfl(rows[u].zb[3], i + 16);
+        const float whole = rows[u].l / (rounded != 0.0f ? rounded : 1.0f);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            // sum p (b + 7.5 s) of group g: rows g and 8 + g of zb, in the lanes j = g / 4 and 2 + g / 4
-            const float mid = __shfl(rows[u].zb[g % 4], i + 16 * (g / 4)) + 7.5f * __shfl(rows[u].zb[g % 4], i + 16 * (2 + g / 4));
+            // sum p (b + 7.5 s) of group g, to p that add up to l: rows g and 8 + g of zb, in the lanes j = g / 4 and 2 + g / 4
+            const float mid = whole * (__shfl(rows[u].zb[g % 4], i + 16 * (g / 4)) + 7.5f * __shfl(rows[u].zb[g % 4], i + 16 * (2 + g / 4)));
             // what the sums of codes are centred by: odd codes by 7.5 sum P',
             // even ones by the mean of 8..15 times it, less 4 of it
             const float4_t z = rows[u].z[g];

@@ -145,6 +145,39 @@ def test_sizes(Q, dt, size):
     check(Q, c, normal((1, 20, 128), dt, 103), tables, np.array([400]), np.array([1]))
 
 
+# ---- offsets: the middles of the groups are large, their spread is small ----
+
+@BOTH
+@pytest.mark.parametrize("n,sharp", [(1, 1.0), (40, 1.0), (40, 30.0), (600, 1.0), (600, 6.0), (600, 30.0)])
+def test_offset_values_of_narrow_groups(Q, dt, n, sharp):
+    """The weights of the middles add up to what they are divided by, whatever the type rounds (one token that comes
+    after the first of its part and takes almost all the weight; many alike)."""
+    print(f"offset {dt} n={n} sharp={sharp}", flush=True)
+    jitter = normal((n, 1, 128), "f16", 112).float()
+    v = (normal((1, 1, 4), "f16", 113).float().repeat_interleave(32, 2) * 20 * (1 + 2.0 ** -9 * jitter)).to(DT[dt])
+    c, tables = cache_of(offset_keys(n, 1, 128, dt, 110), v, 32, dt, [n])
+    for heads in (5, 17):
+        check(Q, c, normal((1, heads, 128), dt, 114), tables, np.array([n]), np.array([1]), scale=sharp / 128 ** 0.5)
+
+
+@BOTH
+@pytest.mark.parametrize("dim,gs", FORMATS)
+def test_offset_values_of_every_format(Q, dt, dim, gs):
+    """As above, 8 tokens whose scores rise by a third of a power of two each."""
+    print(f"offset {dt} D={dim} gs={gs}", flush=True)
+    n, rise = 8, math.log(2) / 3
+    v = (normal((1, 1, dim // gs), "f16", 115).float().repeat_interleave(gs, 2) * 20 *
+         (1 + 2.0 ** -9 * normal((n, 1, dim), "f16", 116).float())).to(DT[dt])
+    k = torch.full((n, 1, dim), 0.0)
+    k[..., :gs] = torch.arange(n)[:, None, None] * rise * 16 / gs
+    c, tables = cache_of(k.to(DT[dt]), v, gs, dt, [n])
+    q = torch.full((1, 3, dim), 1.0)
+    q[0, :, gs:] = 0
+    q[0, 1] *= 0.75
+    q[0, 2] *= 4.5
+    check(Q, c, q.to(DT[dt]), tables, np.array([n]), np.array([1]), scale=1 / 16)
+
+
 # ---- graphs ----
 
 @BOTH
