@@ -352,6 +352,13 @@ struct RowTile {
 template <int DT>
 constexpr float kQsUnit = DT == DT_F16 ? 0x1p-9f : 0x1p-24f;
 
+// Least E, and the one where all scales so far are 0: p itself, up to
+// 2^(8 - E), is an operand as well (fp16) and meets the biases in fp32 sums.
+template <int DT>
+constexpr float kLeastE = DT == DT_F16 ? -6.0f : -100.0f;
+template <int DT>
+constexpr float kFlatE = DT == DT_F16 ? -6.0f : -40.0f;
+
 // 1 as DT, twice.
 template <int DT>
 constexpr uint32_t kOnes = DT == DT_F16 ? 0x3C003C00u : 0x3F803F80u;
@@ -550,11 +557,8 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
 #pragma unroll
         for (int n = 1; n < 16; n *= 2) all = fmaxf(all, __shfl_xor(all, n));
         all = max_j(all);
-        if (all > 0.0f) {
-            // fp16: p itself, up to 2^(8 - E), is an operand as well
-            constexpr float lowest = DT == DT_F16 ? -6.0f : -100.0f;
-            ref_e = fmaxf(ref_e, fminf(fmaxf(static_cast<float>(__builtin_amdgcn_frexp_expf(all)), lowest), 100.0f));
-        }
+        const float e = all > 0.0f ? fminf(static_cast<float>(__builtin_amdgcn_frexp_expf(all)), 100.0f) : kFlatE<DT>;
+        ref_e = fmaxf(ref_e, e);
 #pragma unroll
         for (int u = 0; u < RT; ++u) {
             const float m = fmaxf(rows[u].m, max_j(top[u]));
@@ -883,7 +887,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
 #pragma unroll
         for (int n = 0; n < NT; ++n) rows[u].o[n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    float ref_e = -100.0f;
+    float ref_e = kLeastE<DT>;
 
     // the second of the wavefronts, or workgroups, that share a SIMD
     const bool late = kAttendWaves == 8 ? wave >= 4 : (blockIdx.x & 256) != 0;

@@ -71,11 +71,11 @@ def check(Q, c, q, tables, lens, new, mask=None, scale=None, max_len=None, oracl
     bad = ~(np.abs(g - out) <= tol)
     with np.errstate(invalid="ignore"):
         print(f"  err/bound {np.nanmax(np.abs(g - out) / np.maximum(tol, 1e-300)):.3f}, "
-              f"lse {np.nanmax(np.abs(gl - lse)[seen] / ltol[seen], initial=0):.3f}, "
+              f"lse {np.nanmax(np.abs(gl[seen] - lse[seen]) / ltol[seen], initial=0):.3f}, "
               f"not finite {np.count_nonzero(~np.isfinite(g))}", flush=True)
     assert not bad.any(), f"{np.count_nonzero(bad)} of {bad.size} beyond the bound"
     assert np.array_equal(np.isneginf(gl), ~seen) and (g[~seen] == 0).all()
-    assert (np.abs(gl - lse)[seen] <= ltol[seen]).all()
+    assert (np.abs(gl[seen] - lse[seen]) <= ltol[seen]).all()
     return got, oracle
 
 
@@ -143,6 +143,36 @@ def test_sizes(Q, dt, size):
     k, v = normal((400, 1, 128), dt, 100), (normal((400, 1, 128), dt, 102).float() * size).to(DT[dt])
     c, tables = cache_of(k, v, 64, dt, [400])
     check(Q, c, normal((1, 20, 128), dt, 103), tables, np.array([400]), np.array([1]))
+
+
+# ---- flat groups: scales of 0 ----
+
+@BOTH
+@pytest.mark.parametrize("dim,gs", [(64, 32), (128, 64), (128, 128), (256, 32)])
+@pytest.mark.parametrize("value", ["zero", "constant", "large"])
+def test_flat_values(Q, dt, dim, gs, value):
+    """V constant over each group: everywhere, in one token, in the first 32, in a run of parts."""
+    print(f"flat {dt} D={dim} gs={gs} {value}", flush=True)
+    level = {"zero": 0.0, "constant": 1.0, "large": 3e4 if dt == "f16" else 2.0 ** 24}[value]
+    for n, flat in ((1, [(0, 1)]), (20, [(0, 20)]), (300, [(0, 300)]), (300, [(0, 32)]), (300, [(64, 128), (250, 300)]),
+                    (1500, [(0, 128), (512, 1024)])):
+        k, v = offset_keys(n, 1, dim, dt, 40), normal((n, 1, dim), dt, 42)
+        for a, b in flat:
+            v[a:b] = (level * normal((b - a, 1, dim // gs), dt, 43).float()).clamp(-6e4, 6e4 if dt == "f16" else 1e9).to(
+                DT[dt]).repeat_interleave(gs, 2)
+        c, tables = cache_of(k, v, gs, dt, [n])
+        for heads in (3, 17):
+            check(Q, c, normal((1, heads, dim), dt, 44), tables, np.array([n]), np.array([1]))
+
+
+@BOTH
+def test_flat_head_beside_others(Q, dt):
+    """A kv head of zeros (padding) next to one that holds values; draft trees."""
+    lens, new = np.array([90, 5]), np.array([5, 5])
+    k, v = offset_keys(95, 2, 128, dt, 50), normal((95, 2, 128), dt, 52)
+    k[:, 1], v[:, 1] = 0, 0
+    c, tables = cache_of(k, v, 64, dt, lens)
+    check(Q, c, normal((10, 4, 128), dt, 53), tables, lens, new, mask=np.array([1, 3, 5, 9, 17, 1, 2, 4, 8, 0]))
 
 
 # ---- offsets: the middles of the groups are large, their spread is small ----
