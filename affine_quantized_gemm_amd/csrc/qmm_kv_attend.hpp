@@ -13,10 +13,21 @@
 // the vector ALUs bound this kernel.  The codes are centred because P' is
 // rounded to 11 bits: its error is then weighed by |c - 7.5|, about the size of
 // the values, and not by c; the centring itself is -7.5 sum_t P', a product
-// with a constant.  R = M + E is a running reference: M follows
-// the scores' maximum and E the exponent of the largest s_V, so that P' stays
-// near 1 whatever the values' size.  Both are moved (and everything summed so
-// far scaled) only when a score passes M by 8, or a scale 2^E by 2^7.
+// with a constant.
+//
+// References.  Each row has an R: 6 below its largest score where it was set,
+// rounded up, and moved (what is summed so far scaled) when a score passes it
+// by 11.  P' is an fp16 operand, with 11 bits between 2^-14 and 2^16 and fewer
+// below, so each row and group has an exponent e besides, P' = 2^e p s: 0 if
+// the group's largest p s where R was set is in 2^-4..2^10, else what brings
+// it to about 2^3; moved when a P' passes 2^15.  R and e come from the tokens
+// that the row sees and from nothing else, so that no other token, row or
+// group has a part in a result, whatever its size.
+// As long as the scales of V lie in 2^-9..2^4 all e are 0, and most steps do
+// not know of them.  A wavefront that meets others starts its tokens anew in
+// the form that does (32 sequences of 1k..4k: 48 us instead of 25, 64 rows over 16k 310
+// instead of 120: to know them in every step would cost all calls about 10 %, and to
+// change over in the middle the registers of two forms).
 //
 // Codes as operands.  A 4-bit code in the low bits of an fp16 is the
 // subnormal number c 2^-24 (in bits 4..7: 16 c 2^-24), which the matrix core
@@ -331,20 +342,53 @@ __device__ __forceinline__ void load_step(const uint32_t* rec, const Record& r, 
     }
 }
 
+// An operand of a value per group and lane (16 i, 4 j lanes), and its product:
+// 4 slots a lane are enough for up to 4 groups, and take half the registers.
+template <int G>
+struct Sums {
+    uint32_t v[G == 8 ? 4 : 2];
+};
+template <int DT, int G>
+__device__ __forceinline__ float4_t mfma_sums(const Sums<G>& a, const Sums<G>& b) {
+    const float4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (G == 8) {
+        return mf::mfma<DT>(__builtin_bit_cast(Frag, a), __builtin_bit_cast(Frag, b), zero);
+    } else if constexpr (DT == DT_F16) {
+        typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
+        return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(half4_t, a), __builtin_bit_cast(half4_t, b), zero, 0, 0, 0);
+    } else {
+        typedef short short4_t __attribute__((ext_vector_type(4)));
+        return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(short4_t, a), __builtin_bit_cast(short4_t, b), zero, 0, 0, 0);
+    }
+}
+
+// Heads of 256 in groups of 32: the Q operands lie in LDS behind the slots, a
+// lane's 16 bytes of each side by side (8 KiB a wavefront).  Their registers
+// would have to be spilled, and a wait for a spilled one is a wait for the next
+// step's tokens as well.
+template <int D, int GS>
+constexpr bool kQInLds = D / GS == 8;
+
 // State of one tile of 16 rows.
 template <int D, int GS>
 struct RowTile {
     static constexpr int S = D / 32, G = D / GS, NT = D / 16;
     Frag q[S];        // Q^T operand
-    Frag qs;          // sums of the groups' q, times kQsUnit, in three pieces: slot 8 j + g, piece j; 24 + g: what is lost
+    Sums<G> qs;       // sums of the groups' q, times kQsUnit, in three pieces: group g of lane j, piece j; j = 3: what is lost
     float cs;         // score -> log2 units
-    float m, l;       // M; this lane's share of the sum of p
+    float ref, l;     // R; this lane's share of the sum of p
     float4_t zb;      // sums p b (rows 0..7: group; 7: of p alone, where there are fewer) and p s (rows 8..15)
-    float4_t zp;      // 8 groups: sums of p as zb has it, every row alike
+    float zp;         // 8 groups: this lane's share of the sum of p as zb has it
     float4_t z[G];    // lanes j = 0, 1: sum P'; 2, 3: 4 j + r times it, as a code
     float4_t o[NT];
-    uint64_t bits;    // new tokens that the row sees
 };
+
+// What only some steps need of a row, in LDS.
+struct __attribute__((aligned(16))) RowInfo {
+    uint32_t seen[2];  // bits: new tokens that the row sees
+    uint32_t exps[2];  // e of each group, a byte each
+};
+static_assert(sizeof(RowInfo) == 16, "behind the slots in LDS");
 
 // Unit of the sums of q as an operand.  Scores are in units of 2^-24 q; fp16
 // cannot hold the sums' low bits there (2^-25 would be half a unit of a q
@@ -352,12 +396,23 @@ struct RowTile {
 template <int DT>
 constexpr float kQsUnit = DT == DT_F16 ? 0x1p-9f : 0x1p-24f;
 
-// Least E, and the one where all scales so far are 0: p itself, up to
-// 2^(8 - E), is an operand as well (fp16) and meets the biases in fp32 sums.
-template <int DT>
-constexpr float kLeastE = DT == DT_F16 ? -6.0f : -100.0f;
-template <int DT>
-constexpr float kFlatE = DT == DT_F16 ? -6.0f : -40.0f;
+// Scores may pass R by 11, and scales be up to 2^4 where e is 0, so that P' stays
+// below 2^15.
+constexpr float kScoreRoom = 11.0f, kScaleRoom = 0x1p4f;
+constexpr int kMostSize = 15;
+// e where the row saw no scale but 0 in the group yet.
+constexpr int kNoExp = 127;
+
+__device__ __forceinline__ int exp_of(const RowInfo& info, int g) {
+    return static_cast<int>(info.exps[g / 4] << (24 - 8 * (g % 4))) >> 24;
+}
+// 0 where there is none.
+__device__ __forceinline__ int factor_of(const RowInfo& info, int g) {
+    const int e = exp_of(info, g);
+    return e == kNoExp ? 0 : e;
+}
+// A difference of references as an exponent.
+__device__ __forceinline__ int exp_int(float x) { return static_cast<int>(fminf(fmaxf(x, -300.0f), 300.0f)); }
 
 // 1 as DT, twice.
 template <int DT>
@@ -410,7 +465,7 @@ __device__ __forceinline__ void make_q(RowTile<D, GS>& t, const uint32_t (&w)[D 
 #pragma unroll
         for (int e = 0; e < 4; ++e) t.q[s].v[e] = pack_f16(f[s][e] * up[e & 1], f[s][e + 4] * up[e & 1]);
     }
-    t.qs.v[0] = t.qs.v[1] = t.qs.v[2] = t.qs.v[3] = 0;
+    t.qs = Sums<G>{};
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         const float sum = sum_j(sums[g]) * up[0], x = sum * kQsUnit<DT>;
@@ -458,80 +513,100 @@ __device__ __forceinline__ void priority_rest(bool late) {
     else __builtin_amdgcn_s_setprio(0);
 }
 
-// One step: 32 tokens against the row tiles.  EDGE: `first` is the place of
-// the step's first token among the new ones (negative: before them), `left`
-// how many tokens of the step there are (slots past them may hold anything:
-// their scales and biases of V are taken as 0).
-template <int DT, int D, int GS, int RT, bool EDGE>
-__device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[RT], float& ref_e, int lane,
-                                     int first, int left, bool late) {
+// A step is 32 tokens against the row tiles, in two halves.  EDGE: `first` is
+// the place of the step's first token among the new ones (negative: before
+// them), `left` how many tokens of the step there are (slots past them may hold
+// anything: their scales and biases of V are taken as 0).
+
+// The pair (for 8 groups: pairs n = 0, 1) of V's scales that a lane looks at for
+// the step; `none` stands for tokens past the end.
+template <int D, int GS, bool EDGE>
+__device__ __forceinline__ uint32_t scale_pair(const uint32_t* x, int lane, int n, int left, uint32_t none) {
     using L = Slot<D, GS>;
-    constexpr int S = D / 32, G = D / GS, NT = D / 16, C = D / 64;
+    constexpr int G = L::G;
+    const int at = (lane + 64 * n) % (16 * G);  // (bundle, group), pair
+    uint32_t w = x[L::kVs + (at >> 1) * 4 + (at & 1)];
+    if constexpr (EDGE) {
+        const int tokens = left - (at >> 1) / G * 4 - 2 * (at & 1);
+        const uint32_t keep = tokens >= 2 ? ~0u : tokens == 1 ? 0xFFFFu : 0u;
+        w = (w & keep) | (none & ~keep);
+    }
+    return w;
+}
+
+// The scores, in units 1 / cs; see: which tokens the lane's row sees (EDGE);
+// most: the lane's largest of those.  Returns whether a reference may have to
+// be moved, or a scale is one that e of 0 have no room for.
+template <int DT, int D, int GS, int RT, bool EDGE>
+__device__ __forceinline__ bool step_scores(const uint32_t* x, const RowTile<D, GS> (&rows)[RT], const RowInfo* info, const Frag* q,
+                                            float (&sc)[RT][2][4], bool (&see)[RT][2][4], float (&most)[RT], int lane,
+                                            int first, int left, bool late) {
+    using L = Slot<D, GS>;
+    constexpr int S = D / 32, G = D / GS;
     const int i = lane % 16, j = lane / 16;
     const float4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
 
-    // the largest scale of V, against 2^(E + 7): one or two pairs a lane
-    uint32_t scales[G == 8 ? 2 : 1];
     float big = 0.0f;
 #pragma unroll
     for (int n = 0; n < (G == 8 ? 2 : 1); ++n) {
-        const int at = (lane + 64 * n) % (16 * G);  // (bundle, group), pair
-        scales[n] = x[L::kVs + (at >> 1) * 4 + (at & 1)];
-        if constexpr (EDGE) {
-            const int tokens = left - (at >> 1) / G * 4 - 2 * (at & 1);
-            scales[n] &= tokens >= 2 ? ~0u : tokens == 1 ? 0xFFFFu : 0u;
-        }
-        big = fmaxf(big, fmaxf(half_f32<DT>(scales[n], 0), half_f32<DT>(scales[n], 1)));
+        const uint32_t w = scale_pair<D, GS, EDGE>(x, lane, n, left, 0);
+        big = fmaxf(big, fmaxf(half_f32<DT>(w, 0), half_f32<DT>(w, 1)));
     }
 
     priority_products();
     // scores of all row tiles: sum_g b (sum of q) and s (what the codes' products lose) from the matrix core, + s (codes . q)
-    float sc[RT][2][4];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         uint32_t k[S];
         load_words<S>(x + t * (L::kCodes / 2) + (4 * i + j) * S, k);
-        Frag kb;
-        kb.v[0] = kb.v[1] = kb.v[2] = kb.v[3] = 0;
+        Sums<G> kb{};
         const uint16_t* hb = reinterpret_cast<const uint16_t*>(x + L::kKs) + ((4 * t + i / 4) * G) * 8 + (j < 3 ? 4 : 0) + i % 4;
 #pragma unroll
         for (int g = 0; g < G; ++g) kb.v[g / 2] |= static_cast<uint32_t>(hb[8 * g]) << (16 * (g & 1));
-        float4_t acc[RT], p[RT][G];
+        float4_t acc[RT];
 #pragma unroll
-        for (int u = 0; u < RT; ++u) acc[u] = mf::mfma<DT>(kb, rows[u].qs, zero);
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const Frag a = codes8(k[s]);
-            const int g = 32 * s / GS;
-#pragma unroll
-            for (int u = 0; u < RT; ++u) {
-                if (32 * s % GS == 0) p[u][g] = mf::mfma<DT_F16>(a, rows[u].q[s], zero);
-                else p[u][g] = mf::mfma<DT_F16>(a, rows[u].q[s], p[u][g]);
-            }
-        }
+        for (int u = 0; u < RT; ++u) acc[u] = mfma_sums<DT>(kb, rows[u].qs);
 #pragma unroll
         for (int u = 0; u < RT; ++u)
 #pragma unroll
             for (int r = 0; r < 4; ++r) sc[u][t][r] = DT == DT_F16 ? acc[u][r] * (0x1p-24f / kQsUnit<DT>) : acc[u][r];
+        constexpr int GB = G == 8 ? 4 : G;  // (8 groups: four at a time, for the registers)
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            uint32_t w[2];
-            load_words<2>(x + L::kKs + ((4 * t + j) * G + g) * 4, w);
+        for (int g0 = 0; g0 < G; g0 += GB) {
+            float4_t p[RT][GB];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float ks = half_f32<DT>(w[r / 2], r & 1);
+            for (int s = g0 * GS / 32; s < (g0 + GB) * GS / 32; ++s) {
+                const Frag a = codes8(k[s]);
+                const int g = 32 * s / GS - g0;
 #pragma unroll
-                for (int u = 0; u < RT; ++u) sc[u][t][r] = __builtin_fmaf(ks, p[u][g][r], sc[u][t][r]);
+                for (int u = 0; u < RT; ++u) {
+                    Frag b = rows[u].q[s];
+                    if constexpr (kQInLds<D, GS>) load_words<4>(q[64 * s + lane].v, b.v);
+                    if (32 * s % GS == 0) p[u][g] = mf::mfma<DT_F16>(a, b, zero);
+                    else p[u][g] = mf::mfma<DT_F16>(a, b, p[u][g]);
+                }
             }
+#pragma unroll
+            for (int g = 0; g < GB; ++g) {
+                uint32_t w[2];
+                load_words<2>(x + L::kKs + ((4 * t + j) * G + g0 + g) * 4, w);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float ks = half_f32<DT>(w[r / 2], r & 1);
+#pragma unroll
+                    for (int u = 0; u < RT; ++u) sc[u][t][r] = __builtin_fmaf(ks, p[u][g][r], sc[u][t][r]);
+                }
+            }
+            if constexpr (GB < G) __builtin_amdgcn_sched_barrier(0);
         }
     }
     priority_rest(late);
-    bool see[RT][2][4];
-    float top[RT];
-    bool move = big > exp2_fast(ref_e + 7.0f);
+    bool move = big >= kScaleRoom;
 #pragma unroll
     for (int u = 0; u < RT; ++u) {
         float mx = kFar;
+        uint64_t bits = 0;
+        if constexpr (EDGE) bits = info[16 * u + i].seen[0] | static_cast<uint64_t>(info[16 * u + i].seen[1]) << 32;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -539,57 +614,139 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
                 see[u][t][r] = true;
                 if constexpr (EDGE) {
                     const int at = 16 * t + 4 * j + r, n = first + at;
-                    see[u][t][r] = at < left && (n < 0 || ((rows[u].bits >> (n & 63)) & 1) != 0);
+                    see[u][t][r] = at < left && (n < 0 || ((bits >> (n & 63)) & 1) != 0);
                 }
                 mx = fmaxf(mx, see[u][t][r] ? sc[u][t][r] : kFar);
             }
-        top[u] = mx * rows[u].cs;
-        move = move || top[u] > rows[u].m + 8.0f;
+        most[u] = mx;
+        move = move || mx * rows[u].cs > rows[u].ref + kScoreRoom;
     }
-    if (__any(move)) {
-        const float old_e = ref_e;
-        float all = 0.0f;  // (infinite scales leave the other groups' sums alone)
+    return move;
+}
+
+// Whether all scales of the step lie in 2^-9..2^4: e that are 0 then stay so.
+// (A row's largest p where R was just moved is in 2^5..2^6, so its largest p s
+// lies in 2^-4..2^10; else p s is below 2^15.)
+template <int DT, int D, int GS, bool EDGE>
+__device__ __forceinline__ bool is_calm(const uint32_t* x, int lane, int left) {
+    constexpr int G = D / GS;
+    bool calm = true;
 #pragma unroll
-        for (int n = 0; n < (G == 8 ? 2 : 1); ++n) {
-            const uint32_t w = finite_halves<DT>(scales[n]);
-            all = fmaxf(all, fmaxf(half_f32<DT>(w, 0), half_f32<DT>(w, 1)));
-        }
+    for (int n = 0; n < (G == 8 ? 2 : 1); ++n) {
+        const uint32_t w = scale_pair<D, GS, EDGE>(x, lane, n, left, kOnes<DT>);
 #pragma unroll
-        for (int n = 1; n < 16; n *= 2) all = fmaxf(all, __shfl_xor(all, n));
-        all = max_j(all);
-        const float e = all > 0.0f ? fminf(static_cast<float>(__builtin_amdgcn_frexp_expf(all)), 100.0f) : kFlatE<DT>;
-        ref_e = fmaxf(ref_e, e);
-#pragma unroll
-        for (int u = 0; u < RT; ++u) {
-            const float m = fmaxf(rows[u].m, max_j(top[u]));
-            const float f = exp2_fast(rows[u].m - m + (old_e - ref_e));
-            rows[u].m = m;
-            rows[u].l *= f;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) rows[u].zb[r] *= f;
-            if constexpr (G == 8)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) rows[u].zp[r] *= f;
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) rows[u].z[g][r] *= f;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) rows[u].o[n][r] *= f;
-        }
+        for (int h = 0; h < 2; ++h) calm = calm && half_f32<DT>(w, h) >= 0x1p-9f && half_f32<DT>(w, h) < kScaleRoom;
     }
+    return __all(calm);
+}
+
+// R of a row whose largest score in the step is `high`.
+__device__ __forceinline__ float moved_ref(float from, float high) {
+    return high - from > kScoreRoom ? __builtin_ceilf(high) - 6.0f : from;
+}
+
+// Moves R in a calm step, where all sums of a row scale alike.
+template <int D, int GS, int RT>
+__device__ __forceinline__ void move_calm(RowTile<D, GS> (&rows)[RT], const float (&most)[RT]) {
+    constexpr int G = D / GS, NT = D / 16;
+#pragma unroll
+    for (int u = 0; u < RT; ++u) {
+        const float ref = moved_ref(rows[u].ref, max_j(most[u] > kFar ? most[u] * rows[u].cs : -__builtin_inff()));
+        const float f = __builtin_ldexpf(1.0f, exp_int(rows[u].ref - ref));
+        rows[u].ref = ref;
+        rows[u].l *= f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) rows[u].zb[r] *= f;
+        if constexpr (G == 8) rows[u].zp *= f;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) rows[u].z[g][r] *= f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) rows[u].o[n][r] *= f;
+    }
+}
+
+// Moves R and the e of one tile as the step's scores and scales ask for.  What
+// they become depends on what the row sees and on nothing else.
+template <int DT, int D, int GS>
+__device__ __forceinline__ void move_exact(const uint32_t* x, RowTile<D, GS>& t, RowInfo* info, const float (&sc)[2][4],
+                                           const bool (&see)[2][4], float most, int lane, int left) {
+    using L = Slot<D, GS>;
+    constexpr int G = D / GS;
+    const int i = lane % 16, j = lane / 16;
+    RowInfo mine = info[i];
+    const float from = t.ref;
+    t.ref = moved_ref(from, max_j(most > kFar ? most * t.cs : -__builtin_inff()));
+    const bool up = t.ref != from;
+    const int raised = exp_int(t.ref - from);
+    t.l = __builtin_ldexpf(t.l, -raised);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) t.zb[r] = __builtin_ldexpf(t.zb[r], -raised);
+    if constexpr (G == 8) t.zp = __builtin_ldexpf(t.zp, -raised);
+    float p[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            p[h][r] = see[h][r] ? exp2_fast(__builtin_fmaf(sc[h][r], t.cs, -t.ref)) : 0.0f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        // the largest p s of the row and group (infinite scales count as none)
+        float ps = 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t w[2];
+            load_words<2>(x + L::kVs + ((4 * h + j) * G + g) * 4, w);
+            keep_tokens(w[0], w[1], left - (16 * h + 4 * j));
+            w[0] = finite_halves<DT>(w[0]);
+            w[1] = finite_halves<DT>(w[1]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) ps = fmaxf(ps, p[h][r] * half_f32<DT>(w[r / 2], r & 1));
+        }
+        ps = max_j(ps);
+        const int size = __builtin_amdgcn_frexp_expf(ps);  // 2^(size - 1) <= ps < 2^size
+        const bool none = from == kFar || exp_of(mine, g) == kNoExp;
+        const int kept = exp_of(mine, g) + raised;  // with P' as it was
+        int to = none ? kNoExp : kept < 100 ? kept : 100;
+        if (ps > 0.0f && (up || none || size + kept > kMostSize)) {
+            to = size > 10 || size < -3 ? 3 - size : 0;
+            if (!none && to > 0) to = to < kept ? to : kept > 0 ? kept : 0;  // (the row saw larger ones before)
+            to = to < -126 ? -126 : to > 100 ? 100 : to;
+        }
+        const int scaled = none ? 0 : to - kept;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) t.z[g][r] = __builtin_ldexpf(t.z[g][r], scaled);
+#pragma unroll
+        for (int n = g * (GS / 16); n < (g + 1) * (GS / 16); ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) t.o[n][r] = __builtin_ldexpf(t.o[n][r], scaled);
+        const int at = 8 * (g % 4);
+        mine.exps[g / 4] = (mine.exps[g / 4] & ~(0xFFu << at)) | (static_cast<uint32_t>(to & 0xFF) << at);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    if (j == 0) info[i] = mine;
+}
+
+// p from the scores, its sums, P' and the second product.  PLAIN: all e are 0.
+template <int DT, int D, int GS, int RT, bool EDGE, bool PLAIN>
+__device__ __forceinline__ void step_values(const uint32_t* x, RowTile<D, GS> (&rows)[RT], const RowInfo* info,
+                                            float (&sc)[RT][2][4], const bool (&see)[RT][2][4], int lane, int left,
+                                            bool late) {
+    using L = Slot<D, GS>;
+    constexpr int S = D / 32, G = D / GS, C = D / 64;
+    const int i = lane % 16, j = lane / 16;
     // p, its sum, and p as an operand
     Frag p16[RT];
 #pragma unroll
     for (int u = 0; u < RT; ++u) {
-        const float ref = rows[u].m + ref_e;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                float p = exp2_fast(__builtin_fmaf(sc[u][t][r], rows[u].cs, -ref));
+                float p = exp2_fast(__builtin_fmaf(sc[u][t][r], rows[u].cs, -rows[u].ref));
                 if constexpr (EDGE) p = see[u][t][r] ? p : 0.0f;
                 sc[u][t][r] = p;
                 rows[u].l += p;
@@ -622,12 +779,11 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
         }
 #pragma unroll
         for (int u = 0; u < RT; ++u) rows[u].zb = mf::mfma<DT>(sb, p16[u], rows[u].zb);
-        if constexpr (G == 8) {
-            Frag one;
-            one.v[0] = one.v[1] = one.v[2] = one.v[3] = kOnes<DT>;
+        if constexpr (G == 8)
 #pragma unroll
-            for (int u = 0; u < RT; ++u) rows[u].zp = mf::mfma<DT>(one, p16[u], rows[u].zp);
-        }
+            for (int u = 0; u < RT; ++u)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) rows[u].zp += half_f32<DT>(p16[u].v[k], 0) + half_f32<DT>(p16[u].v[k], 1);
     }
     priority_products();
     // P' and the second product: tile n = 4 c + q of 16 d, from nibble q of the words of quad c
@@ -640,6 +796,17 @@ __device__ __forceinline__ void step(const uint32_t* x, RowTile<D, GS> (&rows)[R
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         Frag pp[RT];
+        if constexpr (!PLAIN) {  // p by this group's 2^e, from the one before's (what falls below fp32 is 2^-26 of the largest p)
+#pragma unroll
+            for (int u = 0; u < RT; ++u) {
+                const RowInfo& mine = info[16 * u + i];
+                const int by = factor_of(mine, g) - (g > 0 ? factor_of(mine, g - 1) : 0);
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) sc[u][t][r] = __builtin_ldexpf(sc[u][t][r], by);
+            }
+        }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             uint32_t w[2];
@@ -856,6 +1023,8 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
         asm volatile("" : "+v"(bits[u]));
     }
     uint32_t* ring = lds + wave * (kAttendSlots * L::kWords);
+    RowInfo* info = reinterpret_cast<RowInfo*>(lds + kAttendWaves * kAttendSlots * L::kWords) + wave * 16 * RT;
+    Frag* q_lds = reinterpret_cast<Frag*>(lds + kAttendWaves * (kAttendSlots * L::kWords + 64 * RT)) + wave * 2 * D;
     const uint32_t ring_at = lds_address(ring);
     constexpr int kStride = ROWS ? 32 : 32 * kAttendWaves;
     // a wavefront without rows (by rows) takes no steps
@@ -871,29 +1040,46 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
     };
     // steps in flight: slot n % kAttendSlots holds step n, `there` whether it has a page (bit 0: the next)
     unsigned there = 0;
+    int slot = 0, t = t_first;
+    auto start = [&] {
+        there = 0;
+        slot = 0;
+        t = t_first;
 #pragma unroll
-    for (int n = 0; n < kAttendSlots - 1; ++n)
-        there |= fetch(t_first + n * kStride, n) ? 1u << n : 0u;
+        for (int n = 0; n < kAttendSlots - 1; ++n)
+            there |= fetch(t_first + n * kStride, n) ? 1u << n : 0u;
+    };
+    start();
     RowTile<D, GS> rows[RT];
 #pragma unroll
     for (int u = 0; u < RT; ++u) {
         make_q<DT, D, GS>(rows[u], qw[u], a.scale, i, j);
-        rows[u].bits = bits[u];
-        rows[u].m = kFar;
-        rows[u].l = 0.0f;
-        rows[u].zb = rows[u].zp = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (kQInLds<D, GS>) {
 #pragma unroll
-        for (int g = 0; g < G; ++g) rows[u].z[g] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int n = 0; n < NT; ++n) rows[u].o[n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int s = 0; s < D / 32; ++s) q_lds[64 * s + lane] = rows[u].q[s];
+        }
+        if (j == 0) info[16 * u + i] = RowInfo{{static_cast<uint32_t>(bits[u]), static_cast<uint32_t>(bits[u] >> 32)}, {0, 0}};
     }
-    float ref_e = kLeastE<DT>;
+    auto clear = [&] {
+#pragma unroll
+        for (int u = 0; u < RT; ++u) {
+            rows[u].ref = wave_row + 16 * u + i < count ? kFar : 0.0f;
+            rows[u].l = 0.0f;
+            rows[u].zp = 0.0f;
+            rows[u].zb = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int g = 0; g < G; ++g) rows[u].z[g] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) rows[u].o[n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+    };
+    clear();
 
     // the second of the wavefronts, or workgroups, that share a SIMD
     const bool late = kAttendWaves == 8 ? wave >= 4 : (blockIdx.x & 256) != 0;
     priority_rest(late);
-    int slot = 0, t = t_first;
-    auto turn = [&](auto edge) {
+    // starts the loads of the step after the one at t and waits for that one's; whether there is any
+    auto begin = [&]() -> bool {
         // the slot that the step before this one was read from
         const int free_slot = slot == 0 ? kAttendSlots - 1 : slot - 1;
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -906,40 +1092,87 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
             if (after == 0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             else if (after == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L::kLoads) : "memory");
             else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * L::kLoads) : "memory");
-            step<DT, D, GS, RT, decltype(edge)::value>(ring + slot * L::kWords, rows, ref_e, lane, t - nt.pos0, t1 - t, late);
         }
+        return have;
+    };
+    auto next = [&] {
         slot = slot == kAttendSlots - 1 ? 0 : slot + 1;
         t += kStride;
     };
+    int calm = 1;
+    // the lane, and where registers are short, one that nothing worked out from it is kept for from step to step
+    auto step_lane = [&]() -> int {
+        int here = lane;
+        if constexpr (RT * G >= 8) asm volatile("" : "+v"(here));
+        return here;
+    };
+    auto turn = [&](auto edge) {
+        constexpr bool EDGE = decltype(edge)::value;
+        if (begin()) {
+            const uint32_t* x = ring + slot * L::kWords;
+            float sc[RT][2][4], most[RT];
+            bool see[RT][2][4];
+            const int here = step_lane();
+            if (__any(step_scores<DT, D, GS, RT, EDGE>(x, rows, info, q_lds, sc, see, most, here, t - nt.pos0, t1 - t, late))) {
+                if (is_calm<DT, D, GS, EDGE>(x, here, t1 - t)) move_calm(rows, most);
+                else calm = 0;
+            }
+            if (calm != 0) step_values<DT, D, GS, RT, EDGE, true>(x, rows, info, sc, see, here, t1 - t, late);
+        }
+        next();
+    };
     // tokens that every row sees, then the new ones and the end
     const int seen = nt.pos0 < t1 ? nt.pos0 : t1;
-    while (t + 32 <= seen) turn(std::false_type{});
-    while (t < t1) turn(std::true_type{});
+    while (calm != 0 && t + 32 <= seen) turn(std::false_type{});
+    while (calm != 0 && t < t1) turn(std::true_type{});
+    if (calm == 0) {
+        // some values are of another size: all over, by the form that can tell
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        load_ids(t0 >> a.s.page_shift);
+        clear();
+        start();
+        while (t < t1) {
+            if (begin()) {
+                const uint32_t* x = ring + slot * L::kWords;
+                float sc[RT][2][4], most[RT];
+                bool see[RT][2][4];
+                step_scores<DT, D, GS, RT, true>(x, rows, info, q_lds, sc, see, most, lane, t - nt.pos0, t1 - t, late);
+#pragma unroll
+                for (int u = 0; u < RT; ++u)
+                    move_exact<DT, D, GS>(x, rows[u], info + 16 * u, sc[u], see[u], most[u], lane, t1 - t);
+                step_values<DT, D, GS, RT, true, false>(x, rows, info, sc, see, lane, t1 - t, late);
+            }
+            next();
+        }
+    }
+    int exps[RT][G];
+#pragma unroll
+    for (int u = 0; u < RT; ++u)
+#pragma unroll
+        for (int g = 0; g < G; ++g) exps[u][g] = factor_of(info[16 * u + i], g);
     if constexpr (!ROWS) __syncthreads();  // the slots become the sums' buffer
 
     // one set of sums: R and l first
-    float bias[RT][G][2], centre[RT][G][2];
+    float middle[RT][G], centre[RT][G][2];
 #pragma unroll
     for (int u = 0; u < RT; ++u) {
         rows[u].l = sum_j(rows[u].l);
         // l over the sum of the rounded p (row 7 of zb: lanes j = 1)
-        const float rounded = G == 8 ? rows[u].zp[0] : __shfl(rows[u].zb[3], i + 16);
+        const float rounded = G == 8 ? sum_j(rows[u].zp) : __shfl(rows[u].zb[3], i + 16);
         const float whole = rows[u].l / (rounded != 0.0f ? rounded : 1.0f);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             // sum p (b + 7.5 s) of group g, to p that add up to l: rows g and 8 + g of zb, in the lanes j = g / 4 and 2 + g / 4
-            const float mid = whole * (__shfl(rows[u].zb[g % 4], i + 16 * (g / 4)) + 7.5f * __shfl(rows[u].zb[g % 4], i + 16 * (2 + g / 4)));
+            middle[u][g] = whole * (__shfl(rows[u].zb[g % 4], i + 16 * (g / 4)) + 7.5f * __shfl(rows[u].zb[g % 4], i + 16 * (2 + g / 4)));
             // what the sums of codes are centred by: odd codes by 7.5 sum P',
-            // even ones by the mean of 8..15 times it, less 4 of it
+            // even ones by the mean of 8..15 times it, less 4 of it (2^-24 each)
             const float4_t z = rows[u].z[g];
             const float codes = z[0] + z[1] + z[2] + z[3], one = __shfl(z[0], i);
-            centre[u][g][0] = 0.125f * (__shfl(codes, i + 32) + __shfl(codes, i + 48));
+            centre[u][g][0] = 0.125f * (__shfl(codes, i + 32) + __shfl(codes, i + 48)) - 0x1p-22f * one;
             centre[u][g][1] = (7.5f * 0x1p-20f) * one;
-            bias[u][g][0] = __builtin_fmaf(4.0f, one, mid);
-            bias[u][g][1] = mid;
         }
         if (!ROWS && j == 0) {
-            stat[wave][u][i][0] = rows[u].l > 0.0f ? rows[u].m + ref_e : kFar;
+            stat[wave][u][i][0] = rows[u].l > 0.0f ? rows[u].ref : kFar;
             stat[wave][u][i][1] = rows[u].l;
         }
     }
@@ -970,8 +1203,8 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
     };
     // value 16 n + 4 j + r of a row, from its three sums
     auto value = [&](int u, int n, int r) {
-        const float up = (n & 1) ? 0x1p20f : 0x1p24f;
-        return __builtin_fmaf(rows[u].o[n][r] - centre[u][16 * n / GS][n & 1], up, bias[u][16 * n / GS][n & 1]);
+        const int g = 16 * n / GS;
+        return __builtin_ldexpf(rows[u].o[n][r] - centre[u][g][n & 1], ((n & 1) ? 20 : 24) - exps[u][g]) + middle[u][g];
     };
     if constexpr (ROWS) {
 #pragma unroll
@@ -985,7 +1218,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
                 const float o[4] = {value(u, n, 0), value(u, n, 1), value(u, n, 2), value(u, n, 3)};
                 put(at, 16 * n + 4 * j, o, inv);
             }
-            if (j == 0) put_lse(at, rows[u].m + ref_e, l);
+            if (j == 0) put_lse(at, rows[u].ref, l);
         }
         return;  // (a sequence is one part)
     } else {
@@ -995,7 +1228,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
 #pragma unroll
             for (int w = 0; w < kAttendWaves; ++w) ref = fmaxf(ref, stat[w][u][i][0]);
             // (a wavefront that saw nothing has l = 0 and sums of 0)
-            const float f = rows[u].l > 0.0f ? exp2_fast(rows[u].m + ref_e - ref) : 0.0f;
+            const float f = rows[u].l > 0.0f ? exp2_fast(rows[u].ref - ref) : 0.0f;
             const int out_row = base_row + 16 * u + oi;
 #pragma unroll
             for (int d0 = 0; d0 < D; d0 += DC) {
@@ -1082,7 +1315,7 @@ template <int DT, int D, int GS, int RT, bool ROWS, bool NT_LOADS>
 hipError_t launch_attend_kernel(const AttendParams& p, dim3 grid, hipStream_t st) {
     constexpr int W = attend_waves(RT, ROWS);
     constexpr int kRow = (D < 128 ? D : 128) + 4;
-    constexpr int slots = 4 * W * kAttendSlots * Slot<D, GS>::kWords;
+    constexpr int slots = 4 * W * (kAttendSlots * Slot<D, GS>::kWords + 64 * RT) + (kQInLds<D, GS> ? 32 * W * D : 0);
     constexpr int sums = 4 * W * (16 * kRow + RT * 16 * 2);
     constexpr int bytes = slots > sums ? slots : sums;
     if constexpr (bytes > 64 * 1024) {

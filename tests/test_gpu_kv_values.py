@@ -175,6 +175,59 @@ def test_flat_head_beside_others(Q, dt):
     check(Q, c, normal((10, 4, 128), dt, 53), tables, lens, new, mask=np.array([1, 3, 5, 9, 17, 1, 2, 4, 8, 0]))
 
 
+# ---- values of very different size ----
+
+OUTLIERS = [("f16", 1e4), ("f16", 6e4), ("bf16", 1e6), ("bf16", 1e20), ("bf16", 1e30)]
+
+
+@pytest.mark.parametrize("dt,size", OUTLIERS)
+@pytest.mark.parametrize("gs", [32, 64, 128])
+@pytest.mark.parametrize("n", [20, 300])
+def test_unseen_outlier_has_no_part(Q, dt, size, gs, n):
+    """A finite draft token of any size: the rows that do not see it are bit for bit as if it were not."""
+    print(f"unseen outlier {dt} {size} gs={gs} n={n}", flush=True)
+    lens, new = np.array([n]), np.array([4])
+    mask = np.array([0b1, 0b11, 0b101, 0b1000])  # the fourth sees the outlier, itself, alone among the new ones
+    k, v, q = offset_keys(n, 1, 128, dt, 60), normal((n, 1, 128), dt, 62), normal((4, 10, 128), dt, 63)
+    got = []
+    for bad in (False, True):
+        if bad:
+            k[n - 1] = (k[n - 1].float() * 100).to(DT[dt])
+            v[n - 1] = (torch.sign(v[n - 1].float()) * (0.5 + 0.5 * torch.rand(1, 128)) * size).to(DT[dt])
+        c, tables = cache_of(k, v, gs, dt, lens)
+        oracle = KO.attend_bound(c, 0, O.to_f64(synth.to_oracle(q), dt), tables, lens, [0, 4], 128 ** -0.5, mask)
+        got.append((check(Q, c, q, tables, lens, new, mask=mask, oracle=oracle)[0], call(Q, c, q, tables, lens, new, mask)[1]))
+    for a, b in zip(*got):
+        assert torch.equal(a[:3].view(torch.uint8), b[:3].view(torch.uint8))
+
+
+@pytest.mark.parametrize("dt,size", OUTLIERS)
+@pytest.mark.parametrize("where", [0, 7, 200, 299])
+def test_outlier_without_weight(Q, dt, size, where):
+    """A token that all rows see with a weight of nothing: it takes no precision from the others."""
+    print(f"weightless outlier {dt} {size} at {where}", flush=True)
+    k, v = normal((300, 1, 128), dt, 70), normal((300, 1, 128), dt, 72)
+    q = (normal((1, 6, 128), dt, 73).float() * 0.3 + 1.0).to(DT[dt])
+    k[where] = -40.0  # scores near -450
+    v[where] = (v[where].float() * size / 4).clamp(-size, size).to(DT[dt])
+    c, tables = cache_of(k, v, 64, dt, [300])
+    check(Q, c, q, tables, np.array([300]), np.array([1]))
+
+
+@pytest.mark.parametrize("dt,big,small", [("f16", 1e4, 1e-2), ("f16", 1e4, 1.0), ("f16", 1.0, 2.0 ** -12),
+                                          ("bf16", 1e10, 1e-10), ("bf16", 1e4, 1.0), ("bf16", 1.0, 1e-12)])
+@pytest.mark.parametrize("dim,gs,heads", [(128, 32, 4), (128, 64, 20), (256, 32, 3)])
+def test_groups_of_different_size(Q, dt, big, small, dim, gs, heads):
+    """Every group keeps its own precision, over a long flat tail of weights too."""
+    print(f"groups {dt} {big}/{small} D={dim} gs={gs} heads={heads}", flush=True)
+    k, v, q = normal((900, 1, dim), dt, 80, 0.5), normal((900, 1, dim), dt, 82).float(), normal((1, heads, dim), dt, 83)
+    v[..., :gs] *= big / 4
+    v[..., gs:] *= small
+    v[0] /= big / small  # the first tokens are smaller in all groups
+    c, tables = cache_of(k, v.to(DT[dt]), gs, dt, [900])
+    check(Q, c, q, tables, np.array([900]), np.array([1]))
+
+
 # ---- offsets: the middles of the groups are large, their spread is small ----
 
 @BOTH
