@@ -400,6 +400,8 @@ constexpr float kQsUnit = DT == DT_F16 ? 0x1p-9f : 0x1p-24f;
 // below 2^15.
 constexpr float kScoreRoom = 11.0f, kScaleRoom = 0x1p4f;
 constexpr int kMostSize = 15;
+// What fp32 sums of p b and p s are to stay below, log2 (bf16 values may be of any size).
+constexpr float kMostSum = 100.0f;
 // e where the row saw no scale but 0 in the group yet.
 constexpr int kNoExp = 127;
 
@@ -680,6 +682,39 @@ __device__ __forceinline__ void move_exact(const uint32_t* x, RowTile<D, GS>& t,
     RowInfo mine = info[i];
     const float from = t.ref;
     t.ref = moved_ref(from, max_j(most > kFar ? most * t.cs : -__builtin_inff()));
+    if constexpr (DT == DT_BF16) {
+        // p times the token's largest bias or 8 scales is to stay below 2^kMostSum: the sums are fp32's (fp16's cannot pass it)
+        float size[2][4], all = 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) size[h][r] = 0.0f;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                uint32_t w[4];
+                load_words<4>(x + L::kVs + ((4 * h + j) * G + g) * 4, w);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float s = half_f32<DT>(finite_halves<DT>(w[r / 2]), r & 1), b = half_f32<DT>(finite_halves<DT>(w[2 + r / 2]), r & 1);
+                    size[h][r] = fmaxf(size[h][r], fmaxf(0.125f * fabsf(b), s));
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if (!see[h][r]) size[h][r] = 0.0f;
+                all = fmaxf(all, size[h][r]);
+            }
+        }
+        if (__any(all > 0x1p64f)) {
+            float high = -__builtin_inff();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (size[h][r] > 0x1p64f) high = fmaxf(high, __builtin_fmaf(sc[h][r], t.cs, __builtin_amdgcn_logf(size[h][r]) + (3.0f - kMostSum)));
+            t.ref = fmaxf(t.ref, __builtin_ceilf(max_j(high)));
+        }
+    }
     const bool up = t.ref != from;
     const int raised = exp_int(t.ref - from);
     t.l = __builtin_ldexpf(t.l, -raised);
@@ -1125,6 +1160,14 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
     const int seen = nt.pos0 < t1 ? nt.pos0 : t1;
     while (calm != 0 && t + 32 <= seen) turn(std::false_type{});
     while (calm != 0 && t < t1) turn(std::true_type{});
+    if constexpr (DT == DT_BF16) {
+        bool small = true;
+#pragma unroll
+        for (int u = 0; u < RT; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) small = small && fabsf(rows[u].zb[r]) < 0x1p99f;
+        if (!__all(small)) calm = 0;
+    }
     if (calm == 0) {
         // some values are of another size: all over, by the form that can tell
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");

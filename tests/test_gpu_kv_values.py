@@ -228,6 +228,30 @@ def test_groups_of_different_size(Q, dt, big, small, dim, gs, heads):
     check(Q, c, q, tables, np.array([900]), np.array([1]))
 
 
+# ---- the ends of the types' ranges ----
+
+@pytest.mark.parametrize("size", [1e30, 1e36, 1e38])
+@pytest.mark.parametrize("kind", ["flat", "spread", "one", "late"])
+@pytest.mark.parametrize("n", [1, 40, 700])
+def test_values_near_the_largest(Q, size, kind, n):
+    """bf16 values near its largest, that carry weight: sums of them are kept below fp32's."""
+    print(f"near the largest {size} {kind} n={n}", flush=True)
+    dt = "bf16"
+    k, v = offset_keys(n, 1, 128, dt, 160), normal((n, 1, 128), dt, 162).float()
+    top = (v / v.abs().max() * size).to(DT[dt]).float()
+    if kind == "flat":
+        v = top[..., :2].repeat_interleave(64, 2)
+    elif kind == "spread":
+        v = top
+    elif kind == "one":
+        v[n // 2] = top[n // 2]
+    else:  # constant groups, of a size that comes after the first steps
+        v = v[..., :2].repeat_interleave(64, 2)
+        v[n // 2:] = top[n // 2:, :, :2].repeat_interleave(64, 2)
+    c, tables = cache_of(k, v.to(DT[dt]), 64, dt, [n])
+    check(Q, c, normal((1, 20, 128), dt, 163), tables, np.array([n]), np.array([1]))
+
+
 # ---- offsets: the middles of the groups are large, their spread is small ----
 
 @BOTH
