@@ -400,6 +400,7 @@ constexpr float kQsUnit = DT == DT_F16 ? 0x1p-9f : 0x1p-24f;
 // below 2^15.
 constexpr float kScoreRoom = 11.0f, kScaleRoom = 0x1p4f;
 constexpr int kMostSize = 15;
+constexpr float kFarScore = 0x1p20f;
 // What fp32 sums of p b and p s are to stay below, log2 (bf16 values may be of any size).
 constexpr float kMostSum = 100.0f;
 // e where the row saw no scale but 0 in the group yet.
@@ -626,13 +627,17 @@ __device__ __forceinline__ bool step_scores(const uint32_t* x, const RowTile<D, 
     return move;
 }
 
-// Whether all scales of the step lie in 2^-9..2^4: e that are 0 then stay so.
+// Whether all scales of the step lie in 2^-9..2^4: e that are 0 then stay so;
+// and no score is one that p_of minds.
 // (A row's largest p where R was just moved is in 2^5..2^6, so its largest p s
 // lies in 2^-4..2^10; else p s is below 2^15.)
-template <int DT, int D, int GS, bool EDGE>
-__device__ __forceinline__ bool is_calm(const uint32_t* x, int lane, int left) {
+template <int DT, int D, int GS, int RT, bool EDGE>
+__device__ __forceinline__ bool is_calm(const uint32_t* x, const RowTile<D, GS> (&rows)[RT], const float (&most)[RT],
+                                        int lane, int left) {
     constexpr int G = D / GS;
     bool calm = true;
+#pragma unroll
+    for (int u = 0; u < RT; ++u) calm = calm && (most[u] == kFar || fabsf(most[u] * rows[u].cs) < kFarScore);
 #pragma unroll
     for (int n = 0; n < (G == 8 ? 2 : 1); ++n) {
         const uint32_t w = scale_pair<D, GS, EDGE>(x, lane, n, left, kOnes<DT>);
@@ -640,6 +645,19 @@ __device__ __forceinline__ bool is_calm(const uint32_t* x, int lane, int left) {
         for (int h = 0; h < 2; ++h) calm = calm && half_f32<DT>(w, h) >= 0x1p-9f && half_f32<DT>(w, h) < kScaleRoom;
     }
     return __all(calm);
+}
+
+// p of a score.  Beyond 2^20 a score is rounded as R was: exactly, the product
+// may lie more above R than fp16 holds.
+template <bool FAR>
+__device__ __forceinline__ float p_of(float score, float cs, float ref) {
+#pragma clang fp contract(off)
+    float x = __builtin_fmaf(score, cs, -ref);
+    if constexpr (FAR) {
+        const float rounded = score * cs;
+        x = fabsf(ref) < kFarScore ? x : rounded - ref;
+    }
+    return exp2_fast(x);
 }
 
 // R of a row whose largest score in the step is `high`.
@@ -726,7 +744,7 @@ __device__ __forceinline__ void move_exact(const uint32_t* x, RowTile<D, GS>& t,
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-            p[h][r] = see[h][r] ? exp2_fast(__builtin_fmaf(sc[h][r], t.cs, -t.ref)) : 0.0f;
+            p[h][r] = see[h][r] ? p_of<true>(sc[h][r], t.cs, t.ref) : 0.0f;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         // the largest p s of the row and group (infinite scales count as none)
@@ -781,7 +799,7 @@ __device__ __forceinline__ void step_values(const uint32_t* x, RowTile<D, GS> (&
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                float p = exp2_fast(__builtin_fmaf(sc[u][t][r], rows[u].cs, -rows[u].ref));
+                float p = p_of<!PLAIN>(sc[u][t][r], rows[u].cs, rows[u].ref);
                 if constexpr (EDGE) p = see[u][t][r] ? p : 0.0f;
                 sc[u][t][r] = p;
                 rows[u].l += p;
@@ -1149,7 +1167,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
             bool see[RT][2][4];
             const int here = step_lane();
             if (__any(step_scores<DT, D, GS, RT, EDGE>(x, rows, info, q_lds, sc, see, most, here, t - nt.pos0, t1 - t, late))) {
-                if (is_calm<DT, D, GS, EDGE>(x, here, t1 - t)) move_calm(rows, most);
+                if (is_calm<DT, D, GS, RT, EDGE>(x, rows, most, here, t1 - t)) move_calm(rows, most);
                 else calm = 0;
             }
             if (calm != 0) step_values<DT, D, GS, RT, EDGE, true>(x, rows, info, sc, see, here, t1 - t, late);

@@ -252,6 +252,24 @@ def test_values_near_the_largest(Q, size, kind, n):
     check(Q, c, normal((1, 20, 128), dt, 163), tables, np.array([n]), np.array([1]))
 
 
+@pytest.mark.parametrize("dt,size", [("f16", 3e3), ("f16", 6e4), ("bf16", 1e5), ("bf16", 1e12)])
+@pytest.mark.parametrize("n", [1, 40, 700])
+def test_scores_beyond_whole_numbers(Q, dt, size, n):
+    """Scores so large that fp32 holds no units of them: the largest, here far ahead, takes all."""
+    print(f"large scores {dt} {size} n={n}", flush=True)
+    k, v, q = normal((n, 1, 128), dt, 170), normal((n, 1, 128), dt, 171), normal((2, 10, 128), dt, 172)
+    k, q = ((x.float() / x.float().abs().max() * size).to(DT[dt]) for x in (k, q))
+    c, tables = cache_of(k, v, 64, dt, [n])
+    q, mask = torch.cat([q, -q]), [0b1000] * 4  # the last token and those before the new ones
+    got, lse = call(Q, c, q, tables, [n], [4], mask=mask)
+    out, want, _, ltol = KO.attend_bound(c, 0, O.to_f64(synth.to_oracle(q), dt), tables, [n], [0, 4], 128 ** -0.5, mask)
+    assert torch.isfinite(got).all() and torch.isfinite(lse).all()
+    g = O.to_f64(synth.to_oracle(got), dt)
+    tie = 2.0 ** -11 if dt == "f16" else 2.0 ** -8
+    assert (np.abs(g - out) <= 2 * tie * np.abs(v.float().numpy()).max()).all()
+    assert (np.abs(lse.cpu().numpy() - want) <= ltol).all()
+
+
 # ---- offsets: the middles of the groups are large, their spread is small ----
 
 @BOTH
