@@ -951,7 +951,7 @@ __device__ __forceinline__ void join_parts(Shared sums, uint32_t at0, uint32_t s
                 for (int e = 0; e < 4; ++e) o[n][e] *= f0;
 #pragma unroll
                 for (int m = 0; m < NP; ++m) {
-                    const float f = s[n][m].y > 0.0f ? exp2_fast(s[n][m].x - top) : 0.0f;
+                    const float f = s[n][m].y != 0.0f ? exp2_fast(s[n][m].x - top) : 0.0f;
                     l[n] = __builtin_fmaf(f, s[n][m].y, l[n]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[n][e] = __builtin_fmaf(f, v[n][m][e], o[n][e]);
@@ -1233,7 +1233,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
             centre[u][g][1] = (7.5f * 0x1p-20f) * one;
         }
         if (!ROWS && j == 0) {
-            stat[wave][u][i][0] = rows[u].l > 0.0f ? rows[u].ref : kFar;
+            stat[wave][u][i][0] = rows[u].l != 0.0f ? rows[u].ref : kFar;
             stat[wave][u][i][1] = rows[u].l;
         }
     }
@@ -1260,7 +1260,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
     };
     auto put_lse = [&](int64_t at, float ref, float l) {
         if (a.lse != nullptr)
-            a.lse[at] = l > 0.0f ? 0.693147180559945f * (ref + __builtin_amdgcn_logf(l)) : -__builtin_inff();
+            a.lse[at] = l != 0.0f ? 0.693147180559945f * (ref + __builtin_amdgcn_logf(l)) : -__builtin_inff();
     };
     // value 16 n + 4 j + r of a row, from its three sums
     auto value = [&](int u, int n, int r) {
@@ -1272,7 +1272,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
         for (int u = 0; u < RT; ++u) {
             const int row = wave_row + 16 * u + i;
             if (row >= count) continue;
-            const float l = rows[u].l, inv = l > 0.0f ? 1.0f / l : 0.0f;
+            const float l = rows[u].l, inv = l != 0.0f ? 1.0f / l : 0.0f;
             const int64_t at = out_at(row);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -1288,8 +1288,8 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
             float ref = kFar;
 #pragma unroll
             for (int w = 0; w < kAttendWaves; ++w) ref = fmaxf(ref, stat[w][u][i][0]);
-            // (a wavefront that saw nothing has l = 0 and sums of 0)
-            const float f = rows[u].l > 0.0f ? exp2_fast(rows[u].ref - ref) : 0.0f;
+            // (a wavefront that saw nothing has l = 0 and sums of 0; an l that is NaN is to show)
+            const float f = rows[u].l != 0.0f ? exp2_fast(rows[u].ref - ref) : 0.0f;
             const int out_row = base_row + 16 * u + oi;
 #pragma unroll
             for (int d0 = 0; d0 < D; d0 += DC) {
@@ -1318,12 +1318,12 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
                 for (int w = 0; w < kAttendWaves; ++w) big = fmaxf(big, stat[w][u][oi][0]);
 #pragma unroll
                 for (int w = 0; w < kAttendWaves; ++w)
-                    l += stat[w][u][oi][1] > 0.0f ? stat[w][u][oi][1] * exp2_fast(stat[w][u][oi][0] - big) : 0.0f;
+                    l += stat[w][u][oi][1] != 0.0f ? stat[w][u][oi][1] * exp2_fast(stat[w][u][oi][0] - big) : 0.0f;
                 if (out_row < count && threadIdx.x < 16 * DC / PER) {
                     if (part.parts == 1) {
                         const int64_t at = out_at(out_row);
 #pragma unroll
-                        for (int e = 0; e < PER; e += 4) put(at, d0 + dd + e, o + e, l > 0.0f ? 1.0f / l : 0.0f);
+                        for (int e = 0; e < PER; e += 4) put(at, d0 + dd + e, o + e, l != 0.0f ? 1.0f / l : 0.0f);
                         if (d0 == 0 && dd == 0) put_lse(at, big, l);
                     } else {
                         const uint32_t at = sums_at(part.slot0 + part.part);
@@ -1331,7 +1331,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
                         for (int e = 0; e < PER; e += 4)
                             store_shared(sums, at + 4 * ((16 * u + oi) * D + d0 + dd + e), float4_t{o[e], o[e + 1], o[e + 2], o[e + 3]});
                         if (d0 == 0 && dd == 0)
-                            store_shared(sums, at + 4 * (16 * RT * D + 4 * (16 * u + oi)), float4_t{l > 0.0f ? big : kFar, l, 0.0f, 0.0f});
+                            store_shared(sums, at + 4 * (16 * RT * D + 4 * (16 * u + oi)), float4_t{l != 0.0f ? big : kFar, l, 0.0f, 0.0f});
                     }
                 }
                 __syncthreads();
@@ -1361,7 +1361,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
     const uint32_t at0 = sums_at(part.slot0), stride = 4 * gridDim.y * a.s.kv_heads * part_floats(D, RT);
     auto finish = [&](int row, int d, const float* o, float ref, float l) {
         const int64_t at = out_at(base_row + row);
-        put(at, d, o, l > 0.0f ? 1.0f / l : 0.0f);
+        put(at, d, o, l != 0.0f ? 1.0f / l : 0.0f);
         if (d == 0) put_lse(at, ref, l);
     };
     // few parts: more items (four values of a row) of a thread in flight

@@ -418,7 +418,8 @@ int qmm_kv_read(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_
  *     the ones up to itself; with mask (int64 [rows], device) instead the
  *     new tokens j whose bit j is set in the row's word (a draft tree: the
  *     row's own token and its ancestors).
- *   - A row that sees nothing gives zeros and lse = -infinity.
+ *   - A row that sees nothing gives zeros and lse = -infinity; one whose scores
+ *     are NaN gives NaN for both.
  *   - What a row does not see has no part in it, infinite or NaN as it may be;
  *     infinite or NaN values that it sees reach their group of the output.
  * fp32 accumulation, softmax and sums; k_hat and v_hat are not rounded; for

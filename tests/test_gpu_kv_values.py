@@ -303,6 +303,32 @@ def test_offset_values_of_every_format(Q, dt, dim, gs):
     check(Q, c, q.to(DT[dt]), tables, np.array([n]), np.array([1]), scale=1 / 16)
 
 
+# ---- NaN ----
+
+@BOTH
+def test_lse_of_nan_scores(Q, dt):
+    """NaN scores give NaN, not the -infinity of a row that sees nothing: one part, several, by rows."""
+    for seqs, n, rows, heads in ((1, 50, 2, 2), (1, 3000, 2, 2), (2, 1000, 5, 8), (40, 40, 18, 8)):
+        print(f"nan scores {dt} seqs={seqs} n={n} rows={rows}", flush=True)
+        k, v = normal((seqs * n, 1, 64), dt, 120), normal((seqs * n, 1, 64), dt, 121)
+        k[n // 2] = float("nan")  # the first sequence only; every row sees it
+        page = 64
+        width = -(-n // page)
+        cache = Q.KVCache.empty(1, seqs * width, 1, 64, 64, page, DT[dt])
+        tables, lens = i32(np.arange(seqs * width).reshape(seqs, width)), i32([n] * seqs)
+        cache.append(0, k.cuda(), v.cuda(), tables, lens)
+        q = normal((seqs * rows, heads, 64), dt, 122)
+        if seqs > 1:
+            q[rows, 0] = float("nan")  # a row of the second
+        out, lse = cache.attend(0, q.cuda(), tables, lens, lse=True, max_len=n)
+        nan = torch.zeros(seqs * rows, heads, dtype=torch.bool)
+        nan[:rows] = True
+        if seqs > 1:
+            nan[rows, 0] = True
+        assert torch.equal(torch.isnan(lse).cpu(), nan) and torch.isfinite(lse[~nan]).all()
+        assert torch.equal(torch.isnan(out).all(-1).cpu(), nan) and torch.isfinite(out[~nan]).all()
+
+
 # ---- graphs ----
 
 @BOTH
