@@ -5,7 +5,10 @@
 //   lo = min, hi = max (a zero minimum is +0),
 //   s  = round_up_dt(fl32(fl32(hi - lo) / 15)),  b = lo,
 //   q  = s == 0 ? 0 : clamp(rint(fl32(fl32(x - b) / s)), 0, 15);
-// back: RNE_dt(fma(s, q, b)).
+// back: RNE_dt(fma(s, q, b)).  Only for NaN it differs: a group that holds one
+// gets NaN for s and b (the weights' quantizer leaves it out of min and max and
+// gives it code 0), so that what a model computed wrongly is not read back as
+// a number.
 //
 // Both kernels give one wavefront a bundle: the four tokens 4u..4u+3 of a
 // page, of one kv head.  That is the unit in which the record keeps V codes
@@ -90,6 +93,10 @@ __device__ __forceinline__ void store_values(uint16_t* p, const uint16_t (&v)[N]
     }
 }
 
+// The smaller and the larger of two, NaN where one of them is.
+__device__ __forceinline__ float low_of(float a, float b) { return __builtin_elementwise_minimum(a, b); }
+__device__ __forceinline__ float high_of(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // Minimum and maximum over runs of LANES lanes (2..16), by exchanges within 16
 // lanes: with the neighbour, the other pair, the other half of 8 (mirrored,
 // its lanes are alike by then), the other 8.
@@ -100,10 +107,10 @@ __device__ __forceinline__ float from_lane(float v) {
 }
 template <int LANES>
 __device__ __forceinline__ void group_min_max(float& lo, float& hi) {
-    if constexpr (LANES >= 2) { lo = fminf(lo, from_lane<0xB1>(lo)); hi = fmaxf(hi, from_lane<0xB1>(hi)); }
-    if constexpr (LANES >= 4) { lo = fminf(lo, from_lane<0x4E>(lo)); hi = fmaxf(hi, from_lane<0x4E>(hi)); }
-    if constexpr (LANES >= 8) { lo = fminf(lo, from_lane<0x141>(lo)); hi = fmaxf(hi, from_lane<0x141>(hi)); }
-    if constexpr (LANES >= 16) { lo = fminf(lo, from_lane<0x140>(lo)); hi = fmaxf(hi, from_lane<0x140>(hi)); }
+    if constexpr (LANES >= 2) { lo = low_of(lo, from_lane<0xB1>(lo)); hi = high_of(hi, from_lane<0xB1>(hi)); }
+    if constexpr (LANES >= 4) { lo = low_of(lo, from_lane<0x4E>(lo)); hi = high_of(hi, from_lane<0x4E>(hi)); }
+    if constexpr (LANES >= 8) { lo = low_of(lo, from_lane<0x141>(lo)); hi = high_of(hi, from_lane<0x141>(hi)); }
+    if constexpr (LANES >= 16) { lo = low_of(lo, from_lane<0x140>(lo)); hi = high_of(hi, from_lane<0x140>(hi)); }
 }
 
 // One operand's N values a lane -> codes; writes the scale and bias of each
@@ -119,8 +126,8 @@ __device__ __forceinline__ void quantize_lane(const uint16_t (&v)[D / 16], uint3
     float lo = f[0], hi = f[0];
 #pragma unroll
     for (int i = 1; i < N; ++i) {
-        lo = fminf(lo, f[i]);
-        hi = fmaxf(hi, f[i]);
+        lo = low_of(lo, f[i]);
+        hi = high_of(hi, f[i]);
     }
     group_min_max<LANES>(lo, hi);
     lo = __fadd_rn(lo, 0.0f);
@@ -148,8 +155,7 @@ __device__ __forceinline__ void quantize_lane(const uint16_t (&v)[D / 16], uint3
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const uint32_t x = static_cast<uint32_t>(t[i]);  // (the conversion saturates)
-        q[i] = x < 15u ? x : 15u;
+        q[i] = static_cast<uint32_t>(__builtin_amdgcn_fmed3f(t[i], 0.0f, 15.0f));  // (of NaN: the least of the others)
     }
     if (live && c % LANES == 0) {
         uint16_t* p = sb + (c / LANES) * 8 + tok;

@@ -390,7 +390,8 @@ int64_t qmm_kv_record_bytes(const qmm_kv_cache* cache);
  * Quantize the new tokens' keys and values into `layer` of the cache.
  * k, v: dt, element (row, head, d) at row * stride_row + head * stride_head
  * + d; base 16-byte aligned, strides (in elements, >= 0) multiples of 8.
- * Bit-exact: the codes, scales and biases are qmm_quantize's.  Other tokens'
+ * Bit-exact: the codes, scales and biases are qmm_quantize's; but a group that
+ * holds a NaN gets a NaN scale and bias, and reads back as NaN.  Other tokens'
  * slots of the same pages are not touched.
  */
 int qmm_kv_append(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_new, int64_t rows,

@@ -329,6 +329,41 @@ def test_lse_of_nan_scores(Q, dt):
         assert torch.equal(torch.isnan(out).all(-1).cpu(), nan) and torch.isfinite(out[~nan]).all()
 
 
+@BOTH
+@pytest.mark.parametrize("dim,gs", FORMATS)
+def test_one_nan_stays_a_nan(Q, dt, dim, gs):
+    """A NaN among finite values: its group reads back as NaN, all else as without it, and attention shows it."""
+    n, kv_heads = 70, 2
+    k, v = normal((n, kv_heads, dim), dt, 130), normal((n, kv_heads, dim), dt, 131)
+    rng = np.random.default_rng(132)
+    places = {(int(rng.integers(n)), int(rng.integers(kv_heads)), d) for d in (0, 7, dim // 2 + 5, dim - 1)}
+    tables, lens = i32([[1, 0]]), i32([n])
+    pools, got = [], []
+    for bad in (False, True):
+        if bad:
+            for t, h, d in places:
+                v[t, h, d] = float("nan")
+        cache = Q.KVCache(torch.zeros(1, 2, kv_heads, Q.record_words(dim, gs, 64, DT[dt]), dtype=torch.int32, device="cuda"),
+                          dim, gs, 64, DT[dt])
+        cache.append(0, k.cuda(), v.cuda(), tables, lens)
+        got.append([x.cpu() for x in cache.read(0, n, tables, lens)])
+        pools.append(cache)
+    group = torch.zeros(n, kv_heads, dim, dtype=torch.bool)
+    for t, h, d in places:
+        group[t, h, d // gs * gs:d // gs * gs + gs] = True
+    assert torch.equal(got[0][0], got[1][0])
+    assert torch.isnan(got[1][1][group]).all() and torch.equal(got[0][1][~group], got[1][1][~group])
+    q = normal((1, 4, dim), dt, 133).cuda()
+    out = [c.attend(0, q, tables, lens).cpu() for c in pools]
+    lost = group.any(0)[None].repeat_interleave(2, 1)
+    assert torch.isnan(out[1][lost]).all()
+    assert torch.equal(out[0][~lost].view(torch.int16), out[1][~lost].view(torch.int16))
+    k[3, 0, 1] = float("nan")  # a key: every score of its head
+    pools[0].append(0, k.cuda(), normal((n, kv_heads, dim), dt, 131).cuda(), tables, lens)
+    out, lse = pools[0].attend(0, q, tables, lens, lse=True)
+    assert torch.isnan(out[:, :2]).all() and torch.isnan(lse[:, :2]).all() and torch.isfinite(out[:, 2:]).all()
+
+
 # ---- graphs ----
 
 @BOTH
