@@ -157,20 +157,24 @@ class KVCache:
         need = self.attend_workspace_bytes(*sizes) if sizes else self._most_space
         return torch.zeros((max(need, 16),), dtype=torch.uint8, device=self.device)
 
-    def _kept_space(self, stream, raw: int):
-        """The workspace kept for the stream, zeroed when made and large enough for every call; a captured call
-        gets one of its own, zeroed in the graph."""
-        capturing = torch.cuda.is_current_stream_capturing()
-        kept = None if capturing else self._spaces.get(raw)
-        if kept is None:
-            if stream is None:
-                kept = torch.zeros((self._most_space,), dtype=torch.uint8, device=self.device)
-            else:
-                with torch.cuda.stream(self._as_stream(stream)):
-                    kept = torch.zeros((self._most_space,), dtype=torch.uint8, device=self.device)
-            if not capturing:
-                self._spaces[raw] = kept
-        return kept
+    def _own_space(self, stream, raw: int, *sizes: int):
+        """Workspace of an :meth:`attend` call that was not given one, and its bytes: the one kept for the stream,
+        zeroed when made and large enough for every call.  A call that is being captured gets one of its own, of the
+        sizes it needs, whose counters are zeroed in the graph; or none where it needs none."""
+        if stream is None:
+            if not torch.cuda.is_current_stream_capturing():
+                kept = self._spaces.get(raw)
+                if kept is None:
+                    kept = self._spaces[raw] = torch.zeros((self._most_space,), dtype=torch.uint8, device=self.device)
+                return kept, self._most_space
+            need = self.attend_workspace_bytes(*sizes)
+            if need == 0:
+                return None, 0
+            own = torch.empty((need,), dtype=torch.uint8, device=self.device)
+            own[:ATTEND_ZEROED_BYTES].zero_()
+            return own, need
+        with torch.cuda.stream(self._as_stream(stream)):  # its state of capture, its memory
+            return self._own_space(None, raw, *sizes)
 
     # ---- tokens ----
 
@@ -238,7 +242,7 @@ class KVCache:
             max_len = max(1, args[6] * self.page_size)
         raw = self._raw(stream)
         if workspace is None:
-            workspace, nbytes = self._kept_space(stream, raw), self._most_space
+            workspace, nbytes = self._own_space(stream, raw, args[2], args[3], rows, heads, max_len)
         else:
             _dev(workspace, "workspace")
             _same_device(q, (workspace, "workspace"))
@@ -246,7 +250,7 @@ class KVCache:
         _check(_lib.qmm_kv_attend(*args, ptr, qr, qh, heads, self._scale if scale is None else scale,
                                   None if mask is None else mask.data_ptr(), out.data_ptr(),
                                   None if lse is False else lse.data_ptr(), max_len,
-                                  workspace.data_ptr(), nbytes, raw), "qmm_kv_attend")
+                                  None if workspace is None else workspace.data_ptr(), nbytes, raw), "qmm_kv_attend")
         return out if lse is False else (out, lse)
 
     # ---- pages ----

@@ -412,3 +412,31 @@ def test_graph_of_a_step_over_real_values(Q, dt):
                                                dim ** -0.5)
             assert (np.abs(O.to_f64(synth.to_oracle(out), dt) - o) <= tol).all()
             assert (np.abs(lse.cpu().numpy() - ls) <= ltol).all()
+
+
+def test_captured_calls_on_a_given_stream(Q):
+    """attend(stream=s) while s is captured and another stream is current: cut into parts and not, against eager calls
+    on that stream between the replays and after them."""
+    dt = "bf16"
+    for n in (60, 2500):
+        print(f"captured stream n={n}", flush=True)
+        c, tables = cache_of(offset_keys(n, 1, 128, dt, 200), normal((n, 1, 128), dt, 201), 64, dt, [n])
+        cache = Q.KVCache(torch.from_numpy(c["pool"].view(np.int32).copy()).cuda(), 128, 64, 64, DT[dt])
+        t, lens = i32(tables), i32([n])
+        q, out = torch.zeros(1, 8, 128, dtype=DT[dt], device="cuda"), torch.zeros(1, 8, 128, dtype=DT[dt], device="cuda")
+        s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            g.capture_begin()
+            with torch.cuda.stream(torch.cuda.Stream()):
+                cache.attend(0, q, t, lens, out=out, stream=s)
+            g.capture_end()
+        for r in range(4):
+            q.copy_(normal(tuple(q.shape), dt, 202 + r))
+            torch.cuda.synchronize()
+            want = cache.attend(0, q, t, lens, stream=s)
+            with torch.cuda.stream(s):
+                g.replay()
+            again = cache.attend(0, q, t, lens, stream=s)
+            torch.cuda.synchronize()
+            assert torch.isfinite(want).all() and torch.equal(want, again) and torch.equal(want, out), r
