@@ -33,16 +33,20 @@ int check_geometry(const qmm_kv_cache* c) {
     return QMM_OK;
 }
 
+// Tokens that a table's row may have room for: positions, and those that a
+// kernel's loops look ahead to, are 32-bit.
+constexpr int64_t kMostTokens = int64_t{1} << 30;
+
 int64_t record_words(const qmm_kv_cache& c) { return Record(c.page_size, c.head_dim, c.group_size).words(); }
 
 // What every call over sequences checks; *s is filled where it returns
-// QMM_OK.  Sizes stay below 2^31 tokens, so that positions are 32-bit.
+// QMM_OK.
 int check_seqs(const qmm_kv_cache* c, int layer, int64_t seqs, int64_t max_new, int64_t rows, const int32_t* tables,
                int64_t width, const int32_t* lens, const int32_t* starts, Seqs* s) {
     if (const int st = check_geometry(c); st != QMM_OK) return st;
     if (layer < 0 || layer >= c->layers || seqs < 0 || max_new < 0 || rows < 0 || width < 0) return QMM_ERR_INVALID_ARG;
     if (seqs > INT32_MAX / 64 || max_new > INT32_MAX / 2 || rows > INT32_MAX ||
-        width > INT32_MAX / c->page_size || max_new > INT32_MAX / c->kv_heads)
+        width > kMostTokens / c->page_size || max_new > INT32_MAX / c->kv_heads)
         return QMM_ERR_UNSUPPORTED;
     if (starts == nullptr && rows != seqs * max_new) return QMM_ERR_INVALID_ARG;
     if (starts != nullptr && rows > seqs * max_new) return QMM_ERR_INVALID_ARG;
@@ -91,7 +95,7 @@ int check_pages(const qmm_kv_cache* c, int64_t seqs, const int32_t* tables, int6
                 const int32_t* refs) {
     if (const int st = check_geometry(c); st != QMM_OK) return st;
     if (seqs < 0 || width < 0) return QMM_ERR_INVALID_ARG;
-    if (seqs > INT32_MAX / 64 || width > INT32_MAX / c->page_size) return QMM_ERR_UNSUPPORTED;
+    if (seqs > INT32_MAX / 64 || width > kMostTokens / c->page_size) return QMM_ERR_UNSUPPORTED;
     if (seqs > 0 && lens != nullptr && off(lens, 4)) return QMM_ERR_MISALIGNED;
     if (seqs > 0 && width > 0)
         if (const int st = check_ptrs({tables}, 4); st != QMM_OK) return st;

@@ -238,7 +238,8 @@ __device__ __forceinline__ Part find_part(const Seqs& s, int unit, int parts, in
     p.chunks = INT32_MAX / kChunk;
     if (parts <= s.seqs) return p;  // one part each
     const int64_t cap = s.width << s.page_shift;
-    int c[kPlanLanes], total = 0;
+    int c[kPlanLanes];
+    uint32_t total = 0;  // (2^8 sequences of up to 2^23 chunks)
 #pragma unroll
     for (int k = 0; k < kPlanLanes; ++k) {
         const int b = 64 * k + lane;
@@ -250,7 +251,7 @@ __device__ __forceinline__ Part find_part(const Seqs& s, int unit, int parts, in
         }
         total += c[k];
     }
-    total = wave_sum(total);
+    total = static_cast<uint32_t>(wave_sum(static_cast<int>(total)));
     // (divisions by T through its fp32 reciprocal: all workgroups do the same, which is all that counts)
     auto parts_at = [&](int k, float inv) {
         return c[k] == 0 ? 0 : static_cast<int>((static_cast<float>(c[k]) - 0.5f) * inv) + 1;

@@ -365,6 +365,9 @@ int qmm_probe_small_m_loop(int dt, int bits, int group_size, int64_t M, int64_t 
  * sequences, at most max_new each.  lens counts them in: row i of sequence b
  * with n new tokens is position lens[b] - n + i.
  *
+ * A row of a table has room for at most 2^30 tokens (table_width * page_size;
+ * QMM_ERR_UNSUPPORTED otherwise).
+ *
  * Every page id, length, start and sequence number read from device memory
  * is checked against the sizes given here before it becomes an address: a
  * position whose table entry names no page of the pool, or that lies outside

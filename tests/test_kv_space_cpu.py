@@ -65,3 +65,22 @@ def test_an_eager_call_while_another_stream_is_captured(cache):
     cache.capturing = {HERE}
     a, n = cache._own_space(THERE, THERE, *LONG)
     assert n == cache._most_space and cache._spaces == {THERE: a}
+
+
+# ---- sizes ----
+
+@pytest.mark.parametrize("page", [32, 64, 128, 256])
+def test_tables_of_more_tokens_than_positions_reach_are_refused(page):
+    """Attention looks up to 256 tokens ahead of a position, in 32 bits: near 2^31 tokens its loops would not end."""
+    L, A, most = Q._lib, 0x10000, (1 << 30) // page  # (addresses are never dereferenced)
+    g = kv.ctypes.byref(kv._Geometry(0, 64, 128, 8, page, 1, 9, A))
+    for width, status in ((most, Q.QMM_ERR_INVALID_ARG), (most + 1, Q.QMM_ERR_UNSUPPORTED),
+                          (((1 << 31) - 1) // page, Q.QMM_ERR_UNSUPPORTED)):
+        # (the width that is served is refused for a NULL operand)
+        assert L.qmm_kv_attend(g, 0, 1, 1, 1, A, width, A, None, None, 128, 128, 8, 1.0, None, A, None, 100, A, 1 << 30, None) == status
+        assert L.qmm_kv_append(g, 0, 1, 1, 1, A, width, A, None, None, 128, 128, A, 128, 128, None) == status
+        assert L.qmm_kv_read(g, 0, 1, 1, 1, A, width, A, None, None, A, None) == status
+        assert L.qmm_kv_reserve(g, 1, A, width, A, A, None, A, A, 1 << 30, None) == status
+        assert L.qmm_kv_fork(g, 1, A, width, A, A, None, A, 1, A, A, 1 << 30, None) == status
+        assert L.qmm_kv_free(g, 1, A, width, A, A, None, 1, None) == status
+        assert L.qmm_kv_compact(g, 1, A, width, A, A, A, None, A, 1 << 30, None) == status
