@@ -648,7 +648,7 @@ __device__ __forceinline__ bool is_calm(const uint32_t* x, const RowTile<D, GS> 
     return __all(calm);
 }
 
-// p of a score.  Beyond 2^20 a score is rounded as R was: exactly, the product
+// p of a score.  Beyond 2^21 a score is rounded as R was: exactly, the product
 // may lie more above R than fp16 holds.
 template <bool FAR>
 __device__ __forceinline__ float p_of(float score, float cs, float ref) {
@@ -656,7 +656,7 @@ __device__ __forceinline__ float p_of(float score, float cs, float ref) {
     float x = __builtin_fmaf(score, cs, -ref);
     if constexpr (FAR) {
         const float rounded = score * cs;
-        x = fabsf(ref) < kFarScore ? x : rounded - ref;
+        x = fabsf(ref) < 2.0f * kFarScore ? x : rounded - ref;  // (an R of the fast form is always below)
     }
     return exp2_fast(x);
 }
@@ -1189,7 +1189,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
     }
     if (calm == 0) {
         // some values are of another size: all over, by the form that can tell
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");  // (no slot is written or read any more)
         load_ids(t0 >> a.s.page_shift);
         clear();
         start();
