@@ -186,10 +186,12 @@ __device__ __forceinline__ void store_k(uint32_t* row, const uint32_t (&q)[D / 1
     }
 }
 
-// 4 prompts of 1801..2047 tokens, 8 heads of 128 (fp16, 36 MB) 15.2 us, 2.4
-// TB/s: the vector ALUs bound it, 406 instructions a wavefront of 4 tokens.  64
-// tokens of 64 sequences 4.8 us, 4..6 rows of 16 sequences (heads of 256) 5.4: a launch
-// and two dependent reads (length, page).
+// 4 prompts of 1801..2047 tokens, 8 heads of 128 (fp16, 40 MB) 15.1 us, 2.7
+// TB/s; neither memory nor the vector ALUs (47 % busy, 406 instructions a
+// wavefront of 4 tokens) are full: of the wavefronts' time 20 % goes to instructions,
+// 44 % to waits for data and barriers, 37 % to waits for a unit.  64 tokens of 64
+// sequences 4.7 us, 4..6 rows of 16 sequences (heads of 256) 5.3: a launch and two
+// dependent reads (length, page).
 template <int DT, int D, int GS>
 __global__ __launch_bounds__(64 * kWaves) void append_kernel(Seqs s, const uint16_t* __restrict__ k,
                                                              int64_t k_row, int64_t k_head,
@@ -254,7 +256,7 @@ __global__ __launch_bounds__(64 * kWaves) void append_kernel(Seqs s, const uint1
     }
 }
 
-// The way back: the same prompts 10.7 us, 3.4 TB/s; the small calls 3.6 and 3.9.
+// The way back: the same prompts 10.8 us, 3.7 TB/s; the small calls 3.6 and 3.8.
 template <int DT, int D, int GS>
 __global__ __launch_bounds__(64 * kWaves) void read_kernel(Seqs s, uint16_t* __restrict__ k,
                                                            uint16_t* __restrict__ v) {

@@ -25,11 +25,11 @@ struct AttendPlan {
 // tokens a start, a meeting of its wavefronts and an end for every two tiles:
 // over sequences, kv heads and pairs of tiles, as multiples of the
 // workgroups that the chip runs at a time, those weigh as
-// 512 * multiple > max_len + 384.  Measured (us, by rows / by tokens, 64
-// rows of 4 heads of 128): multiple 1/16, 512 tokens 20.7 / 14.4; 1, 128
-// 10.4 / 11.4 and 512 22.0 / 13.9; 2, 128 10.8 / 20.9, 512 22.7 / 26.2 and
-// 1024 38.9 / 33.2; 4, 1024 43.3 / 64.8 and 4096 143 / 144.  64 rows of 32
-// heads over 16k tokens 142 / 118.
+// 512 * multiple > max_len + 384.  Measured (us of a call, by rows / by tokens,
+// 64 rows of 4 heads of 128): multiple 1/16, 512 tokens 21.5 / 15.5; 1, 128
+// 11.3 / 13.4 and 512 22.3 / 16.6; 2, 128 12.2 / 24.1, 512 23.0 / 30.4 and
+// 1024 37.1 / 37.6; 4, 1024 45.5 / 71.6 and 4096 175 / 185.  64 rows of 32
+// heads, 4 sequences of 16k 639 / 117.
 // Parts for the workgroups that fill the chip over the kv heads and row
 // groups; where the sequences are that many, or short, or too many to plan,
 // one part each.

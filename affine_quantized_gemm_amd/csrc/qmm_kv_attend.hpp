@@ -10,7 +10,7 @@
 // again.  Nothing is ever dequantized, and what remains besides the codes --
 // biases of K against sums of q, sums of p b and p s -- are small products
 // of the stored scales and biases as they are, on the matrix cores as well:
-// the vector ALUs bound this kernel.  The codes are centred because P' is
+// the vector ALUs are its busiest unit.  The codes are centred because P' is
 // rounded to 11 bits: its error is then weighed by |c - 7.5|, about the size of
 // the values, and not by c; the centring itself is -7.5 sum_t P', a product
 // with a constant.
@@ -25,9 +25,11 @@
 // group has a part in a result, whatever its size.
 // As long as the scales of V lie in 2^-9..2^4 all e are 0, and most steps do
 // not know of them.  A wavefront that meets others starts its tokens anew in
-// the form that does (32 sequences of 1k..4k: 48 us instead of 25, 64 rows over 16k 310
-// instead of 120: to know them in every step would cost all calls about 10 %, and to
-// change over in the middle the registers of two forms).
+// the form that does (32 sequences of 1k..4k: 49 us instead of 25, 64 rows over
+// 16k 310 instead of 120).  To know them in every step is one more instruction
+// for every probability and group, 32 of 320 with two tiles; to change over in
+// the middle takes the registers of two forms, and a spilled one is a wait for
+// the next tokens (verify rows 69 us and more instead of 41).
 //
 // Codes as operands.  A 4-bit code in the low bits of an fp16 is the
 // subnormal number c 2^-24 (in bits 4..7: 16 c 2^-24), which the matrix core
@@ -510,7 +512,8 @@ __device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
 // SIMD's two wavefronts do not do their softmax at the same time; between
 // them the younger wavefront (`late`) goes first, which otherwise falls behind
 // and is left without another to hide its waits.  (64 rows over 16k tokens
-// 118 us, 131 without; verify rows over 8k 39.4, 41.2.)
+// 121 us, 128 without; 32 sequences of 1k..4k 25.4, 27.4; verify rows over 8k
+// 41.5, 42.7.)
 __device__ __forceinline__ void priority_products() { __builtin_amdgcn_s_setprio(2); }
 __device__ __forceinline__ void priority_rest(bool late) {
     if (late) __builtin_amdgcn_s_setprio(1);
@@ -997,16 +1000,17 @@ __device__ __forceinline__ void join_parts(Shared sums, uint32_t at0, uint32_t s
 // group blockIdx.y (row = new token * group + head within the group).
 //
 // Measured (bf16 or fp16, 32 heads, 8 kv heads of 128, groups of 64 unless
-// said): one token over 777 tokens 9.9 us, 32 sequences of 1k..4k 24.9 us
-// (3.8 TB/s; 13.7 us of reading), 16 sequences of 4..6 rows over 8k 40.3 us
-// (3.7 TB/s; 21.6), one token over 131071 30.5 us (4.7 TB/s; 20.6), 64 rows of
-// 4 sequences over 16k 120 us (546 TFLOP/s; 54; 111 in
-// a row of calls); 8 trees of 13 rows, 16 heads
-// of 64, up to 2k 11.8 us.  A call starts (lengths, plan, q, page ids, first
-// tokens) in 3 to 4 us and joins its parts in about 4; between them one row tile
-// is bound by its reads (6 TB/s over 131071 tokens), two by the vector ALUs:
-// 320 instructions a step of 32 tokens for operands out of codes, scaling the
-// scores, the softmax and P' (64 rows: 63 % busy, the matrix cores 28 %).
+// said): one token over 777 tokens 10.1 us, 32 sequences of 1k..4k 25.3 us
+// (3.8 TB/s; 13.7 us of reading), 16 sequences of 4..6 rows over 8k 41.7 us
+// (3.6 TB/s; 21.6), one token over 131071 30.7 us (4.6 TB/s; 20.6), 64 rows of
+// 4 sequences over 16k 121 us (542 TFLOP/s; 54; 111 in a row of calls); 8 trees
+// of 13 rows, 16 heads of 64, up to 2k 12.6 us.  A call starts (lengths, plan,
+// q, page ids, first tokens) in 3 to 4 us and joins its parts in about 4;
+// between them one row tile is bound by its reads (6 TB/s over 131071 tokens).
+// With two no unit is full: vector ALUs 52 % busy (verify rows) and 63 % (64
+// rows), matrix cores 18 % and 28 %; of the wavefronts' time, two a SIMD,
+// 49 % and 51 % goes to instructions, 30 % and 23 % to waits for data, 21 %
+// and 26 % to waits for a unit.
 template <int DT, int D, int GS, int RT, bool ROWS, bool NT_LOADS>
 __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT)) void attend_kernel(AttendParams a) {
     constexpr int kAttendWaves = attend_waves(RT, ROWS), kTiles = attend_tiles(RT, ROWS);
@@ -1391,9 +1395,10 @@ hipError_t launch_attend_kernel(const AttendParams& p, dim3 grid, hipStream_t st
 }
 
 // Tokens that workgroups of several row groups read stay in L2; others are
-// streamed past it (one token over 131071: 30.4 us, kept 35.1).  Heads of 256,
-// four row groups, 64 sequences of 4096 tokens: 162 us, streamed 192; of 128,
-// eight row groups over 16k either way 116.
+// streamed past it (one token over 131071: 30.7 us, kept 35.1).  Heads of 256,
+// four row groups, 4096 tokens: 64 sequences of 4 heads 195 us, streamed 216, 16
+// of 8 heads 84 and 96; of 64 sequences of 8 heads, 604 MB, 448 and 422.  Heads
+// of 128, eight row groups over 16k: either way 120.
 template <int DT, int D, int GS>
 hipError_t run_attend(const AttendParams& p, int row_tiles, bool by_rows, dim3 grid, hipStream_t st) {
     if constexpr (D <= 128) {

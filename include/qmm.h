@@ -426,10 +426,14 @@ int qmm_kv_read(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_
  *     are NaN gives NaN for both.
  *   - What a row does not see has no part in it, infinite or NaN as it may be;
  *     infinite or NaN values that it sees reach their group of the output.
- * fp32 accumulation, softmax and sums; k_hat and v_hat are not rounded; for
+ * fp32 accumulation, softmax and sums; k_hat and v_hat are not rounded.  For
  * the second product the probabilities times the scale of their value are
- * rounded to fp16 (11 bits, either dt), for the biases to dt; one rounding to
- * dt at the end.  Deterministic.
+ * rounded to fp16, either dt, in units of their own row and group (11 bits
+ * down to 2^-10 of the largest, 2^-21 of it below); for what the biases and
+ * 7.5 times the scales add, the probabilities are rounded to dt, and the sum
+ * of the rounded ones divides it; one rounding to dt at the end.
+ * Deterministic.  Values of V may be of any size; where their scales leave
+ * 2^-9..2^4 a call takes about twice as long.
  *
  * max_len: no sequence is longer (1..table_width * page_size); it bounds how
  * many parts the sequences are cut into.  Longer ones are still attended to
