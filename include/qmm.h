@@ -417,7 +417,8 @@ int qmm_kv_read(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_
  * [rows][heads] (fp32, natural logarithm of the sum of exponentials).
  *   - heads is a multiple of kv_heads; heads h*heads/kv_heads .. share kv
  *     head h.  1 <= max_new <= 64.
- *   - q as k in qmm_kv_append.  Scores are scale * q . k_hat.
+ *   - q as k in qmm_kv_append, of values below 2^105 in size.  Scores are
+ *     scale * q . k_hat.
  *   - A row sees every token before its sequence's new ones, and of these
  *     the ones up to itself; with mask (int64 [rows], device) instead the
  *     new tokens j whose bit j is set in the row's word (a draft tree: the

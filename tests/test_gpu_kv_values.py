@@ -228,6 +228,37 @@ def test_groups_of_different_size(Q, dt, big, small, dim, gs, heads):
     check(Q, c, q, tables, np.array([900]), np.array([1]))
 
 
+@BOTH
+@pytest.mark.parametrize("dim,gs", [(64, 32), (128, 32), (128, 64), (256, 32), (256, 64)])
+def test_sizes_by_rows(Q, dt, dim, gs):
+    """Workgroups by rows: a head of zeros, one of small values, one with a large group, an ordinary one; ragged rows."""
+    print(f"sizes by rows {dt} D={dim} gs={gs}", flush=True)
+    lens, new = np.array([40 + b % 9 for b in range(40)]), np.array([18 - b % 3 for b in range(40)])
+    n = int(lens.sum())
+    k, v = offset_keys(n, 4, dim, dt, 104), normal((n, 4, dim), dt, 106).float()
+    v[:, 0] = 0
+    v[:, 1] *= 2.0 ** -13
+    v[:, 2, :gs] *= 2.0 ** 10
+    c, tables = cache_of(k, v.to(DT[dt]), gs, dt, lens)
+    check(Q, c, normal((int(new.sum()), 8, dim), dt, 107), tables, lens, new, max_len=48)
+
+
+@BOTH
+def test_sizes_beside_holes(Q, dt):
+    """Steps without a page, before, between and after those of unusual size; cut into parts and not."""
+    print(f"sizes beside holes {dt}", flush=True)
+    n = 1500
+    k, v = offset_keys(n, 1, 128, dt, 108), normal((n, 1, 128), dt, 109).float()
+    v[200:700] *= 2.0 ** -14
+    v[900:1000] = 0
+    c, tables = cache_of(k, v.to(DT[dt]), 64, dt, [n])
+    tables[0, [0, 4, 5, 12, 23]] = -1
+    tables[0, 8] = 999
+    q = normal((2, 10, 128), dt, 110)
+    _, oracle = check(Q, c, q, tables, np.array([n]), np.array([2]))
+    check(Q, c, q, tables, np.array([n]), np.array([2]), max_len=32, oracle=oracle)
+
+
 # ---- the ends of the types' ranges ----
 
 @pytest.mark.parametrize("size", [1e30, 1e36, 1e38])
