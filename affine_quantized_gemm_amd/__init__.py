@@ -39,6 +39,9 @@ EXPORTS = (
     "qmm_kv_record_bytes", "qmm_kv_append", "qmm_kv_read", "qmm_kv_attend", "qmm_kv_attend_workspace_bytes",
     "qmm_kv_pages_workspace_bytes", "qmm_kv_copy_pages", "qmm_kv_reserve", "qmm_kv_fork", "qmm_kv_free",
     "qmm_kv_compact",
+    "qmm_gated", "qmm_gated_backward", "qmm_gated_backward_workspace_bytes", "qmm_rotary", "qmm_log_probs",
+    "qmm_log_probs_needs_workspace", "qmm_log_probs_backward", "qmm_kv_attend_window",
+    "qmm_kv_attend_window_workspace_bytes",
 )
 NOALLOC_SCRATCH_BYTES = 8 * 1024 * 1024  # QMM_NOALLOC_SCRATCH_BYTES
 
@@ -97,12 +100,24 @@ def _load():
         "qmm_kv_attend_workspace_bytes": (i64, [vp, i64, i64, i64, i64, i64]),
         "qmm_kv_attend": (i32, [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, i64, i64, i64, ctypes.c_float, vp, vp, vp,
                                 i64, vp, i64, vp]),
+        "qmm_kv_attend_window_workspace_bytes": (i64, [vp, i64, i64, i64, i64, i64, i64, i64]),
+        "qmm_kv_attend_window": (i32, [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, i64, i64, i64, ctypes.c_float, vp, i64,
+                                       i64, vp, vp, i64, vp, i64, vp]),
         "qmm_kv_pages_workspace_bytes": (i64, [vp, i64]),
         "qmm_kv_copy_pages": (i32, [vp, vp, vp, i64, vp]),
         "qmm_kv_reserve": (i32, [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp]),
         "qmm_kv_fork": (i32, [vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, i64, vp]),
         "qmm_kv_free": (i32, [vp, i64, vp, i64, vp, vp, vp, i64, vp]),
         "qmm_kv_compact": (i32, [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp]),
+        "qmm_gated": (i32, [i32, i32, i32, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp]),
+        "qmm_gated_backward_workspace_bytes": (i64, [i32, i32, i32, i64, i64, i64]),
+        "qmm_gated_backward": (i32, [i32, i32, i32, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp]),
+        "qmm_rotary": (i32, [i32, i64, i64, i64, i64, i32, i32, ctypes.c_float, vp, i64, i64, vp, i32, i64, i32, vp, vp, vp,
+                             i64, i64, vp]),
+        "qmm_log_probs_needs_workspace": (i32, [i64, i64]),
+        "qmm_log_probs": (i32, [i32, i64, i64, ctypes.c_float, vp, i64, vp, i32, i64, i64, vp, vp, vp, vp, vp, vp, i64, vp]),
+        "qmm_log_probs_backward": (i32, [i32, i64, i64, ctypes.c_float, vp, i64, vp, i32, i64, vp, vp, vp, vp, vp, vp, i64,
+                                         vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -484,3 +499,5 @@ def small_m_noalloc(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor, bia
 
 
 from .kv import KVCache, record_words  # noqa: E402,F401  (needs the definitions above)
+from .rows import (LogProbs, gated, gated_backward, gated_backward_workspace_bytes, log_probs,  # noqa: E402,F401
+                   log_probs_backward, log_probs_workspace, rotary)

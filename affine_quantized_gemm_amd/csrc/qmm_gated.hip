@@ -1,0 +1,114 @@
+// Gated block on quantized weights: how a call is split, and its launch.
+#include "qmm_gated.hpp"
+#include "qmm_gated_dx.hpp"
+
+namespace qmm {
+namespace gated {
+
+template <> GatedFn gated_fn<DT_F16, 4>(int);
+template <> GatedFn gated_fn<DT_F16, 6>(int);
+template <> GatedFn gated_fn<DT_F16, 8>(int);
+template <> GatedFn gated_fn<DT_BF16, 4>(int);
+template <> GatedFn gated_fn<DT_BF16, 6>(int);
+template <> GatedFn gated_fn<DT_BF16, 8>(int);
+template <> DxFn dx_fn<DT_F16, 4>(int);
+template <> DxFn dx_fn<DT_F16, 6>(int);
+template <> DxFn dx_fn<DT_F16, 8>(int);
+template <> DxFn dx_fn<DT_BF16, 4>(int);
+template <> DxFn dx_fn<DT_BF16, 6>(int);
+template <> DxFn dx_fn<DT_BF16, 8>(int);
+
+}  // namespace gated
+
+hipError_t launch_gated(const GatedArgs& a) {
+    using namespace gated;
+    GatedParams p{};
+    p.x = static_cast<const uint16_t*>(a.x);
+    p.wq = a.wq;
+    p.scales = static_cast<const uint16_t*>(a.scales);
+    p.biases = static_cast<const uint16_t*>(a.biases);
+    p.grad = static_cast<const uint16_t*>(a.grad);
+    p.out = static_cast<uint16_t*>(a.out);
+    p.d = a.d;
+    p.M = static_cast<int>(a.M);
+    p.act = a.act;
+    p.F = a.F;
+    p.K = a.K;
+    p.words = static_cast<int>(a.K * a.bits / 32);
+    p.groups = static_cast<int>(a.K / a.gs);
+    p.supers = static_cast<int>((a.K + kSuper - 1) / kSuper);
+    const bool vec = a.K % kSuper == 0;
+    const int rt = !vec || a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
+    const int row_blocks = static_cast<int>((a.M + 16 * rt - 1) / (16 * rt));
+    const int rows = static_cast<int>(a.M < 16 * rt ? a.M : 16 * rt);
+    const int64_t tiles16 = (a.F + 15) / 16;
+    // shares of K until the wavefronts fill the chip; x of all shares goes through LDS together
+    const int most = kChunkBytes / (2 * rows * kSuper);  // superblocks of x in LDS
+    const int64_t fill = rt <= 2 ? 4096 : 2048;
+    while ((2 << p.ks_shift) <= kWaves && (2 << p.ks_shift) <= most && (1 << p.ks_shift) < p.supers &&
+           (tiles16 << p.ks_shift) * row_blocks < fill)
+        ++p.ks_shift;
+    const int ks = 1 << p.ks_shift;
+    const int whole = (p.supers + ks - 1) / ks * ks, part = most / ks * ks;
+    p.chunk = kSuper * (whole < part ? whole : part);
+    p.chunks = (p.supers * kSuper + p.chunk - 1) / p.chunk;
+    const int64_t tiles = (tiles16 * ks + kWaves - 1) / kWaves;
+    if (tiles > INT32_MAX / 2) return hipErrorInvalidValue;
+    p.tiles = static_cast<int>(tiles);
+    // workgroups that the chip holds at a time; a multiple of 8, so that the row blocks of a column share an XCD's L2
+    const int64_t hold = 512;
+    const int64_t grid_x = tiles < hold ? (tiles + 7) / 8 * 8 : hold;
+    const int bytes = lds_bytes(rows, p.chunk, p.chunks, a.gs, rt);
+    const dim3 grid(static_cast<unsigned>(grid_x), static_cast<unsigned>(row_blocks));
+    GatedFn fn = nullptr;
+    const bool half = a.dt == DT_F16;
+    switch (a.bits) {
+        case 4: fn = half ? gated_fn<DT_F16, 4>(a.gs) : gated_fn<DT_BF16, 4>(a.gs); break;
+        case 6: fn = half ? gated_fn<DT_F16, 6>(a.gs) : gated_fn<DT_BF16, 6>(a.gs); break;
+        case 8: fn = half ? gated_fn<DT_F16, 8>(a.gs) : gated_fn<DT_BF16, 8>(a.gs); break;
+        default: break;
+    }
+    return fn != nullptr ? fn(p, rt, vec, grid, bytes, a.stream) : hipErrorInvalidValue;
+}
+
+// Slices for the workgroups that the chip holds at a time: two a CU with one
+// row tile, else one.
+GatedDxPlan gated_dx_plan(int64_t M, int64_t F, int64_t K) {
+    using namespace gated;
+    const int64_t blocks = (K + kDxCols - 1) / kDxCols, chunks = (2 * F + kDxRows - 1) / kDxRows;
+    int64_t slices = (M <= 16 ? 512 : 256) / blocks;
+    slices = slices < 1 ? 1 : slices < chunks ? slices : chunks;
+    const int64_t slice = (chunks + slices - 1) / slices * kDxRows;
+    return {static_cast<int>((2 * F + slice - 1) / slice), slice};
+}
+
+hipError_t launch_gated_dx(const GatedArgs& a, void* y, float* part) {
+    using namespace gated;
+    const GatedDxPlan plan = gated_dx_plan(a.M, a.F, a.K);
+    DxParams p{};
+    p.d = a.d;
+    p.wq = a.wq;
+    p.scales = static_cast<const uint16_t*>(a.scales);
+    p.biases = static_cast<const uint16_t*>(a.biases);
+    p.y = static_cast<uint16_t*>(y);
+    p.part = part;
+    p.M = static_cast<int>(a.M);
+    p.N = 2 * a.F;
+    p.K = a.K;
+    p.slice = plan.slice;
+    const dim3 grid(static_cast<unsigned>((a.K + kDxCols - 1) / kDxCols), static_cast<unsigned>(plan.slices));
+    DxFn fn = nullptr;
+    const bool half = a.dt == DT_F16;
+    switch (a.bits) {
+        case 4: fn = half ? dx_fn<DT_F16, 4>(a.gs) : dx_fn<DT_BF16, 4>(a.gs); break;
+        case 6: fn = half ? dx_fn<DT_F16, 6>(a.gs) : dx_fn<DT_BF16, 6>(a.gs); break;
+        case 8: fn = half ? dx_fn<DT_F16, 8>(a.gs) : dx_fn<DT_BF16, 8>(a.gs); break;
+        default: break;
+    }
+    if (fn == nullptr) return hipErrorInvalidValue;
+    const hipError_t e = fn(p, static_cast<int>((a.M + 15) / 16), grid, a.stream);
+    if (e != hipSuccess || plan.slices == 1) return e;
+    return launch_reduce_partials(a.dt, part, y, plan.slices, a.M * a.K, a.stream);
+}
+
+}  // namespace qmm

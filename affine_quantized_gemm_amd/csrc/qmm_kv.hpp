@@ -81,10 +81,11 @@ struct AttendArgs {
     float* lse;
     void* workspace;
     int64_t max_len;
+    int window, sinks;  // window 0: none
     hipStream_t stream;
 };
 int64_t attend_workspace(const qmm_kv_cache& c, int64_t seqs, int64_t max_new, int64_t rows, int64_t heads,
-                         int64_t max_len);
+                         int64_t max_len, int window, int sinks);
 hipError_t launch_attend(const qmm_kv_cache& c, const AttendArgs& a);
 
 struct PageArgs {

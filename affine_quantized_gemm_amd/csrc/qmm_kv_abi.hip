@@ -137,21 +137,35 @@ int qmm_kv_read(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_
     return hip_status(launch_read(*cache, s, k, v, static_cast<hipStream_t>(stream)));
 }
 
-int64_t qmm_kv_attend_workspace_bytes(const qmm_kv_cache* cache, int64_t seqs, int64_t max_new, int64_t rows,
-                                      int64_t heads, int64_t max_len) {
+// (a window beyond the longest sequence is none)
+static int clamped(int64_t n) { return static_cast<int>(n < kMostTokens ? n : kMostTokens); }
+
+static int64_t attend_space(const qmm_kv_cache* cache, int64_t seqs, int64_t max_new, int64_t rows, int64_t heads,
+                            int64_t max_len, int window, int sinks) {
     if (const int st = check_geometry(cache); st != QMM_OK) return st;
     if (seqs < 0 || max_new < 0 || rows < 0 || max_len < 1) return QMM_ERR_INVALID_ARG;
     if (seqs > INT32_MAX / 64 || rows > INT32_MAX || max_len > INT32_MAX) return QMM_ERR_UNSUPPORTED;
     if (const int st = check_heads(cache, max_new, heads); st != QMM_OK) return st;
     if (rows == 0 || max_new == 0) return 0;
-    return attend_workspace(*cache, seqs, max_new, rows, heads, max_len);
+    return attend_workspace(*cache, seqs, max_new, rows, heads, max_len, window, sinks);
 }
 
-int qmm_kv_attend(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_new, int64_t rows,
+int64_t qmm_kv_attend_workspace_bytes(const qmm_kv_cache* cache, int64_t seqs, int64_t max_new, int64_t rows,
+                                      int64_t heads, int64_t max_len) {
+    return attend_space(cache, seqs, max_new, rows, heads, max_len, 0, 0);
+}
+
+int64_t qmm_kv_attend_window_workspace_bytes(const qmm_kv_cache* cache, int64_t seqs, int64_t max_new, int64_t rows,
+                                             int64_t heads, int64_t max_len, int64_t window, int64_t sinks) {
+    if (window < 1 || sinks < 0) return QMM_ERR_INVALID_ARG;
+    return attend_space(cache, seqs, max_new, rows, heads, max_len, clamped(window), clamped(sinks));
+}
+
+static int attend(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_new, int64_t rows,
                   const int32_t* tables, int64_t table_width, const int32_t* lens, const int32_t* starts,
                   const void* q, int64_t q_stride_row, int64_t q_stride_head, int64_t heads, float scale,
                   const int64_t* mask, void* out, float* lse, int64_t max_len, void* workspace,
-                  int64_t workspace_bytes, void* stream) {
+                  int64_t workspace_bytes, int window, int sinks, void* stream) {
     Seqs s{};
     int st = check_seqs(cache, layer, seqs, max_new, rows, tables, table_width, lens, starts, &s);
     if (st != QMM_OK) return st;
@@ -163,11 +177,30 @@ int qmm_kv_attend(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t ma
     if ((st = check_ptrs({out}, 16)) != QMM_OK) return st;
     if (off(mask, 8) || off(lse, 4)) return QMM_ERR_MISALIGNED;
     st = check_workspace(workspace, workspace_bytes,
-                         attend_workspace(*cache, seqs, max_new, rows, heads, max_len));
+                         attend_workspace(*cache, seqs, max_new, rows, heads, max_len, window, sinks));
     if (st != QMM_OK) return st;
     return hip_status(launch_attend(
         *cache, AttendArgs{s, Rows{q, q_stride_row, q_stride_head}, static_cast<int>(heads), scale, mask, out, lse,
-                           workspace, max_len, static_cast<hipStream_t>(stream)}));
+                           workspace, max_len, window, sinks, static_cast<hipStream_t>(stream)}));
+}
+
+int qmm_kv_attend(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_new, int64_t rows,
+                  const int32_t* tables, int64_t table_width, const int32_t* lens, const int32_t* starts,
+                  const void* q, int64_t q_stride_row, int64_t q_stride_head, int64_t heads, float scale,
+                  const int64_t* mask, void* out, float* lse, int64_t max_len, void* workspace,
+                  int64_t workspace_bytes, void* stream) {
+    return attend(cache, layer, seqs, max_new, rows, tables, table_width, lens, starts, q, q_stride_row, q_stride_head,
+                  heads, scale, mask, out, lse, max_len, workspace, workspace_bytes, 0, 0, stream);
+}
+
+int qmm_kv_attend_window(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_new, int64_t rows,
+                         const int32_t* tables, int64_t table_width, const int32_t* lens, const int32_t* starts,
+                         const void* q, int64_t q_stride_row, int64_t q_stride_head, int64_t heads, float scale,
+                         const int64_t* mask, int64_t window, int64_t sinks, void* out, float* lse, int64_t max_len,
+                         void* workspace, int64_t workspace_bytes, void* stream) {
+    if (window < 1 || sinks < 0) return QMM_ERR_INVALID_ARG;
+    return attend(cache, layer, seqs, max_new, rows, tables, table_width, lens, starts, q, q_stride_row, q_stride_head,
+                  heads, scale, mask, out, lse, max_len, workspace, workspace_bytes, clamped(window), clamped(sinks), stream);
 }
 
 int64_t qmm_kv_pages_workspace_bytes(const qmm_kv_cache* cache, int64_t n) {

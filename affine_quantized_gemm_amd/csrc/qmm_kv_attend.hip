@@ -4,12 +4,18 @@
 namespace qmm {
 namespace kv {
 
-template <> AttendFn attend_fn<DT_F16, 64>(int);
-template <> AttendFn attend_fn<DT_F16, 128>(int);
-template <> AttendFn attend_fn<DT_F16, 256>(int);
-template <> AttendFn attend_fn<DT_BF16, 64>(int);
-template <> AttendFn attend_fn<DT_BF16, 128>(int);
-template <> AttendFn attend_fn<DT_BF16, 256>(int);
+template <> AttendFn attend_fn<DT_F16, 64, false>(int);
+template <> AttendFn attend_fn<DT_F16, 64, true>(int);
+template <> AttendFn attend_fn<DT_F16, 128, false>(int);
+template <> AttendFn attend_fn<DT_F16, 128, true>(int);
+template <> AttendFn attend_fn<DT_F16, 256, false>(int);
+template <> AttendFn attend_fn<DT_F16, 256, true>(int);
+template <> AttendFn attend_fn<DT_BF16, 64, false>(int);
+template <> AttendFn attend_fn<DT_BF16, 64, true>(int);
+template <> AttendFn attend_fn<DT_BF16, 128, false>(int);
+template <> AttendFn attend_fn<DT_BF16, 128, true>(int);
+template <> AttendFn attend_fn<DT_BF16, 256, false>(int);
+template <> AttendFn attend_fn<DT_BF16, 256, true>(int);
 
 namespace {
 
@@ -54,15 +60,32 @@ AttendPlan plan_of(const qmm_kv_cache& c, int64_t seqs, int64_t max_new, int64_t
     return p;
 }
 
+// Tokens that the rows of a sequence may see, up to whole steps at both ends.
+int64_t seen_len(int64_t max_new, int64_t max_len, int window, int sinks) {
+    const int64_t most = static_cast<int64_t>(window) + sinks + max_new + 96;
+    return window > 0 && most < max_len ? most : max_len;
+}
+
+template <bool WINDOW>
+AttendFn attend_of(const qmm_kv_cache& c) {
+    const bool half = c.dt == QMM_F16;
+    switch (c.head_dim) {
+        case 64: return half ? attend_fn<DT_F16, 64, WINDOW>(c.group_size) : attend_fn<DT_BF16, 64, WINDOW>(c.group_size);
+        case 128: return half ? attend_fn<DT_F16, 128, WINDOW>(c.group_size) : attend_fn<DT_BF16, 128, WINDOW>(c.group_size);
+        case 256: return half ? attend_fn<DT_F16, 256, WINDOW>(c.group_size) : attend_fn<DT_BF16, 256, WINDOW>(c.group_size);
+        default: return nullptr;
+    }
+}
+
 }  // namespace
 
 int64_t attend_workspace(const qmm_kv_cache& c, int64_t seqs, int64_t max_new, int64_t, int64_t heads,
-                         int64_t max_len) {
-    return plan_of(c, seqs, max_new, heads, max_len).bytes;
+                         int64_t max_len, int window, int sinks) {
+    return plan_of(c, seqs, max_new, heads, seen_len(max_new, max_len, window, sinks)).bytes;
 }
 
 hipError_t launch_attend(const qmm_kv_cache& c, const AttendArgs& a) {
-    const AttendPlan p = plan_of(c, a.s.seqs, a.s.max_new, a.heads, a.max_len);
+    const AttendPlan p = plan_of(c, a.s.seqs, a.s.max_new, a.heads, seen_len(a.s.max_new, a.max_len, a.window, a.sinks));
     AttendParams k{};
     k.s = a.s;
     k.q = static_cast<const uint16_t*>(a.q.p);
@@ -72,6 +95,8 @@ hipError_t launch_attend(const qmm_kv_cache& c, const AttendArgs& a) {
     k.group = a.heads / c.kv_heads;
     k.parts = p.parts;
     k.scale = a.scale;
+    k.window = a.window;
+    k.sinks = a.sinks;
     k.mask = a.mask;
     k.out = static_cast<uint16_t*>(a.out);
     k.lse = a.lse;
@@ -80,14 +105,7 @@ hipError_t launch_attend(const qmm_kv_cache& c, const AttendArgs& a) {
     const int64_t blocks = (static_cast<int64_t>(p.parts) * c.kv_heads + 7) / 8 * 8;
     if (blocks > INT32_MAX || p.row_groups > 65535) return hipErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(p.row_groups));
-    AttendFn fn = nullptr;
-    const bool half = c.dt == QMM_F16;
-    switch (c.head_dim) {
-        case 64: fn = half ? attend_fn<DT_F16, 64>(c.group_size) : attend_fn<DT_BF16, 64>(c.group_size); break;
-        case 128: fn = half ? attend_fn<DT_F16, 128>(c.group_size) : attend_fn<DT_BF16, 128>(c.group_size); break;
-        case 256: fn = half ? attend_fn<DT_F16, 256>(c.group_size) : attend_fn<DT_BF16, 256>(c.group_size); break;
-        default: break;
-    }
+    const AttendFn fn = a.window > 0 ? attend_of<true>(c) : attend_of<false>(c);
     return fn != nullptr ? fn(k, p.row_tiles, p.by_rows, grid, a.stream) : hipErrorInvalidValue;
 }
 

@@ -107,6 +107,7 @@ struct AttendParams {
     // where sequences are cut: how many parts of (sequence, row group, head) are done, and the parts' sums
     uint32_t* done;         // [seqs][row_groups][kv_heads], kDoneStride apart, 0 before and after the call
     float* sums;            // [parts][row_groups][kv_heads][part_floats]
+    int window, sinks;      // (forms with a window)
 };
 
 // Floats of one part's sums: rows of D values, then (R, l, -, -) of each row.
@@ -226,11 +227,60 @@ struct Part {
     int b, part, parts, first, chunks, slot0;  // slot0: number of the sequence's first part
 };
 
+// With a window a sequence's steps are taken in another order, and those that
+// no row sees not at all: first the steps that all rows see whole (among the
+// sinks, then from where the last row's window surely begins to the new
+// tokens), then the others (the sinks' last, the window's begin, the new
+// ones).  So there is one loop for each form of a step, as without a window;
+// a branch in one loop, a third loop or a loop around two had up to 370
+// registers spilled.  Positions are counted in this order; each of the five
+// pieces lies `by` further on in the sequence.
+struct Window {
+    int len;         // tokens of all pieces
+    int all;         // of those that all rows see
+    int end[4], by[5];
+    __device__ __forceinline__ int real(int t) const {
+        return t + (t < end[0] ? by[0] : t < end[1] ? by[1] : t < end[2] ? by[2] : t < end[3] ? by[3] : by[4]);
+    }
+};
+__device__ __forceinline__ Window window_of(const NewTokens& nt, int64_t cap, int window, int sinks) {
+    auto down = [](int t) { return t & ~31; };
+    auto up = [](int t) { return (t + 31) & ~31; };
+    auto least = [](int x, int y) { return x < y ? x : y; };
+    auto most = [](int x, int y) { return x > y ? x : y; };
+    const int len = most(0, static_cast<int>(nt.pos0 + nt.n < cap ? nt.pos0 + nt.n : cap));
+    const int before = most(0, least(nt.pos0, len));
+    const int sinks_whole = down(least(sinks, before)), sinks_end = least(up(least(sinks, len)), len);
+    const int low = down(most(0, nt.pos0 - window));           // no row sees what is before it, and no sink
+    const int whole = most(up(most(0, nt.pos0 + nt.n - window)), sinks_whole);  // (a row sees at most nt.n new ones)
+    const int fresh = most(down(before), 0);
+    // pieces: begin and tokens
+    const bool some = whole < fresh;
+    const int n1 = some ? fresh - whole : 0;
+    const int n2 = some ? most(0, least(sinks_end, whole) - sinks_whole) : sinks_end - sinks_whole;
+    const int b3 = most(low, sinks_end), n3 = most(0, (some ? whole : len) - b3);
+    const int n4 = some ? len - fresh : 0;
+    Window w;
+    w.all = sinks_whole + n1;
+    w.end[0] = sinks_whole;
+    w.end[1] = w.all;
+    w.end[2] = w.all + n2;
+    w.end[3] = w.end[2] + n3;
+    w.len = w.end[3] + n4;
+    w.by[0] = 0;
+    w.by[1] = whole - w.end[0];
+    w.by[2] = sinks_whole - w.end[1];
+    w.by[3] = b3 - w.end[2];
+    w.by[4] = fresh - w.end[3];
+    return w;
+}
+
 // Every sequence gets ceil(chunks / T) parts with the least T (up to where
 // the search stops) for which they are at most `parts` together: all
 // workgroups then take about T chunks whatever the lengths are.  Each
 // workgroup finds the cut by itself from the lengths, 64 a register.
-__device__ __forceinline__ Part find_part(const Seqs& s, int unit, int parts, int lane) {
+template <bool WINDOW>
+__device__ __forceinline__ Part find_part(const Seqs& s, int unit, int parts, int lane, int window, int sinks) {
     Part p;
     p.part = 0;
     p.parts = 1;
@@ -247,7 +297,8 @@ __device__ __forceinline__ Part find_part(const Seqs& s, int unit, int parts, in
         const int b = 64 * k + lane;
         c[k] = 0;
         if (64 * k < s.seqs && b < s.seqs) {
-            const int64_t len = s.lens[b];
+            int64_t len = s.lens[b];
+            if constexpr (WINDOW) len = window_of(new_tokens(s, b), cap, window, sinks).len;
             c[k] = static_cast<int>(((len < cap ? len : cap) + kChunk - 1) / kChunk);
             c[k] = c[k] > 0 ? c[k] : 1;
         }
@@ -385,6 +436,23 @@ struct RowTile {
     float4_t z[G];    // lanes j = 0, 1: sum P'; 2, 3: 4 j + r times it, as a code
     float4_t o[NT];
 };
+
+// The new tokens (bits) that a row sees under a window: it keeps the last
+// `window` of the tokens it sees and those before position `sinks`.  low: the
+// first token before the new ones that it sees, from there (0 or less).
+__device__ __forceinline__ uint64_t window_bits(uint64_t bits, const NewTokens& nt, int window, int sinks, int& low) {
+    // (bits that name no token do not count)
+    if (nt.n < 64) bits &= (uint64_t{1} << nt.n) - 1;
+    const int pos0 = nt.pos0;
+    if (pos0 < 0) bits = pos0 > -64 ? bits >> -pos0 << -pos0 : 0;
+    const int count = __builtin_popcountll(bits);
+    low = count < window ? count - window : 0;
+    uint64_t last = bits;
+    for (int n = count - window; n > 0; --n) last &= last - 1;  // (at most 63 rounds)
+    const int first = sinks - pos0;  // new tokens that are sinks
+    const uint64_t firsts = first <= 0 ? 0 : first >= 64 ? ~uint64_t{0} : (uint64_t{1} << first) - 1;
+    return last | (bits & firsts);
+}
 
 // What only some steps need of a row, in LDS.
 struct __attribute__((aligned(16))) RowInfo {
@@ -541,13 +609,14 @@ __device__ __forceinline__ uint32_t scale_pair(const uint32_t* x, int lane, int 
     return w;
 }
 
+// WINDOW: sinks, counted as first; lows: what window_bits found for each row.
 // The scores, in units 1 / cs; see: which tokens the lane's row sees (EDGE);
 // most: the lane's largest of those.  Returns whether a reference may have to
 // be moved, or a scale is one that e of 0 have no room for.
-template <int DT, int D, int GS, int RT, bool EDGE>
-__device__ __forceinline__ bool step_scores(const uint32_t* x, const RowTile<D, GS> (&rows)[RT], const RowInfo* info, const Frag* q,
-                                            float (&sc)[RT][2][4], bool (&see)[RT][2][4], float (&most)[RT], int lane,
-                                            int first, int left, bool late) {
+template <int DT, int D, int GS, int RT, bool EDGE, bool WINDOW>
+__device__ __forceinline__ bool step_scores(const uint32_t* x, const RowTile<D, GS> (&rows)[RT], const RowInfo* info, const int* lows,
+                                            const Frag* q, float (&sc)[RT][2][4], bool (&see)[RT][2][4], float (&most)[RT], int lane,
+                                            int first, int sinks, int left, bool late) {
     using L = Slot<D, GS>;
     constexpr int S = D / 32, G = D / GS;
     const int i = lane % 16, j = lane / 16;
@@ -614,6 +683,8 @@ __device__ __forceinline__ bool step_scores(const uint32_t* x, const RowTile<D, 
         float mx = kFar;
         uint64_t bits = 0;
         if constexpr (EDGE) bits = info[16 * u + i].seen[0] | static_cast<uint64_t>(info[16 * u + i].seen[1]) << 32;
+        int low = 0;
+        if constexpr (EDGE && WINDOW) low = lows[16 * u + i];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -621,7 +692,10 @@ __device__ __forceinline__ bool step_scores(const uint32_t* x, const RowTile<D, 
                 see[u][t][r] = true;
                 if constexpr (EDGE) {
                     const int at = 16 * t + 4 * j + r, n = first + at;
-                    see[u][t][r] = at < left && (n < 0 || ((bits >> (n & 63)) & 1) != 0);
+                    if constexpr (WINDOW)
+                        see[u][t][r] = at < left && (n < 0 ? n >= low || n < sinks : ((bits >> (n & 63)) & 1) != 0);
+                    else
+                        see[u][t][r] = at < left && (n < 0 || ((bits >> (n & 63)) & 1) != 0);
                 }
                 mx = fmaxf(mx, see[u][t][r] ? sc[u][t][r] : kFar);
             }
@@ -1011,7 +1085,7 @@ __device__ __forceinline__ void join_parts(Shared sums, uint32_t at0, uint32_t s
 // rows), matrix cores 18 % and 28 %; of the wavefronts' time, two a SIMD,
 // 49 % and 51 % goes to instructions, 30 % and 23 % to waits for data, 21 %
 // and 26 % to waits for a unit.
-template <int DT, int D, int GS, int RT, bool ROWS, bool NT_LOADS>
+template <int DT, int D, int GS, int RT, bool ROWS, bool NT_LOADS, bool WINDOW>
 __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT)) void attend_kernel(AttendParams a) {
     constexpr int kAttendWaves = attend_waves(RT, ROWS), kTiles = attend_tiles(RT, ROWS);
     using L = Slot<D, GS>;
@@ -1028,7 +1102,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
     // heads fastest; workgroups that read the same tokens (row groups, blockIdx.y) are a multiple of 8 apart: one XCD
     const uint32_t unit = blockIdx.x / static_cast<uint32_t>(a.s.kv_heads);
     const int head = static_cast<int>(blockIdx.x - unit * a.s.kv_heads), rg = blockIdx.y;
-    const Part part = find_part(a.s, static_cast<int>(unit), a.parts, lane);
+    const Part part = find_part<WINDOW>(a.s, static_cast<int>(unit), a.parts, lane, a.window, a.sinks);
     const int b = part.b;
     if (b < 0) return;
     const NewTokens nt = new_tokens(a.s, b);
@@ -1037,7 +1111,11 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
     if (base_row >= count) return;
     const int wave_row = base_row + (ROWS ? wave * 16 * RT : 0);  // the wavefront's first
     const int64_t cap = a.s.width << a.s.page_shift;
-    const int len = static_cast<int>(nt.pos0 + nt.n < cap ? nt.pos0 + nt.n : cap);
+    Window win{};
+    if constexpr (WINDOW) win = window_of(nt, cap, a.window, a.sinks);
+    const int len = WINDOW ? win.len : static_cast<int>(nt.pos0 + nt.n < cap ? nt.pos0 + nt.n : cap);
+    // (positions are counted in the window's order up to where the record, or the place among the new tokens, counts)
+    auto real = [&](int t) { return WINDOW ? win.real(t) : t; };
     const int t0 = part.first * kChunk;
     const int t1 = len - t0 > part.chunks * kChunk ? t0 + part.chunks * kChunk : len;
 
@@ -1051,10 +1129,10 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
         ids = c < a.s.width ? a.s.tables[static_cast<int64_t>(b) * a.s.width + c] : -1;
         if (ids >= a.s.pages) ids = -1;
     };
-    load_ids(t0 >> a.s.page_shift);
+    load_ids(real(t0) >> a.s.page_shift);
     auto page_at = [&](int t) -> int {
         const int col = t >> a.s.page_shift;
-        if (col >= col0 + 64) load_ids(col);
+        if (WINDOW ? static_cast<unsigned>(col - col0) >= 64 : col >= col0 + 64) load_ids(col);
         return __builtin_amdgcn_readlane(ids, col - col0);
     };
     // the rows of q, asked for together with the page ids; worked on while the first tokens come
@@ -1083,6 +1161,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
     uint32_t* ring = lds + wave * (kAttendSlots * L::kWords);
     RowInfo* info = reinterpret_cast<RowInfo*>(lds + kAttendWaves * kAttendSlots * L::kWords) + wave * 16 * RT;
     Frag* q_lds = reinterpret_cast<Frag*>(lds + kAttendWaves * (kAttendSlots * L::kWords + 64 * RT)) + wave * 2 * D;
+    int* lows = reinterpret_cast<int*>(lds) + kAttendWaves * (kAttendSlots * L::kWords + 64 * RT + (kQInLds<D, GS> ? 8 * D : 0)) + wave * 16 * RT;
     const uint32_t ring_at = lds_address(ring);
     constexpr int kStride = ROWS ? 32 : 32 * kAttendWaves;
     // a wavefront without rows (by rows) takes no steps
@@ -1090,10 +1169,11 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
     // starts the loads of the step at token t; whether there are any
     auto fetch = [&](int t, int slot) -> bool {
         if (t >= t1) return false;
-        const int page = page_at(t);
+        const int at = real(t);
+        const int page = page_at(at);
         if (page < 0) return false;
         const uint32_t* r = a.s.pool + (static_cast<int64_t>(page) * a.s.kv_heads + head) * rec.words();
-        load_step<D, GS, NT_LOADS>(r, rec, t & mask_slot, lane, ring_at + 4 * slot * L::kWords);
+        load_step<D, GS, NT_LOADS>(r, rec, at & mask_slot, lane, ring_at + 4 * slot * L::kWords);
         return true;
     };
     // steps in flight: slot n % kAttendSlots holds step n, `there` whether it has a page (bit 0: the next)
@@ -1115,6 +1195,11 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
         if constexpr (kQInLds<D, GS>) {
 #pragma unroll
             for (int s = 0; s < D / 32; ++s) q_lds[64 * s + lane] = rows[u].q[s];
+        }
+        if constexpr (WINDOW) {
+            int low;
+            bits[u] = window_bits(bits[u], nt, a.window, a.sinks, low);
+            if (j == 0) lows[16 * u + i] = low;
         }
         if (j == 0) info[16 * u + i] = RowInfo{{static_cast<uint32_t>(bits[u]), static_cast<uint32_t>(bits[u] >> 32)}, {0, 0}};
     }
@@ -1171,7 +1256,8 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
             float sc[RT][2][4], most[RT];
             bool see[RT][2][4];
             const int here = step_lane();
-            if (__any(step_scores<DT, D, GS, RT, EDGE>(x, rows, info, q_lds, sc, see, most, here, t - nt.pos0, t1 - t, late))) {
+            if (__any(step_scores<DT, D, GS, RT, EDGE, WINDOW>(x, rows, info, lows, q_lds, sc, see, most, here, real(t) - nt.pos0,
+                                                               a.sinks - nt.pos0, t1 - t, late))) {
                 if (is_calm<DT, D, GS, RT, EDGE>(x, rows, most, here, t1 - t)) move_calm(rows, most);
                 else calm = 0;
             }
@@ -1180,7 +1266,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
         next();
     };
     // tokens that every row sees, then the new ones and the end
-    const int seen = nt.pos0 < t1 ? nt.pos0 : t1;
+    const int all_seen = WINDOW ? win.all : nt.pos0, seen = all_seen < t1 ? all_seen : t1;
     while (calm != 0 && t + 32 <= seen) turn(std::false_type{});
     while (calm != 0 && t < t1) turn(std::true_type{});
     if constexpr (DT == DT_BF16) {
@@ -1194,7 +1280,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
     if (calm == 0) {
         // some values are of another size: all over, by the form that can tell
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");  // (no slot is written or read any more)
-        load_ids(t0 >> a.s.page_shift);
+        load_ids(real(t0) >> a.s.page_shift);
         clear();
         start();
         while (t < t1) {
@@ -1202,7 +1288,8 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
                 const uint32_t* x = ring + slot * L::kWords;
                 float sc[RT][2][4], most[RT];
                 bool see[RT][2][4];
-                step_scores<DT, D, GS, RT, true>(x, rows, info, q_lds, sc, see, most, lane, t - nt.pos0, t1 - t, late);
+                step_scores<DT, D, GS, RT, true, WINDOW>(x, rows, info, lows, q_lds, sc, see, most, lane, real(t) - nt.pos0,
+                                                         a.sinks - nt.pos0, t1 - t, late);
 #pragma unroll
                 for (int u = 0; u < RT; ++u)
                     move_exact<DT, D, GS>(x, rows[u], info + 16 * u, sc[u], see[u], most[u], lane, t1 - t);
@@ -1377,20 +1464,21 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
     else join_parts<D, RT, W, 1, 12>(sums, at0, stride, part.parts, valid, meet, finish);
 }
 
-template <int DT, int D, int GS, int RT, bool ROWS, bool NT_LOADS>
+template <int DT, int D, int GS, int RT, bool ROWS, bool NT_LOADS, bool WINDOW>
 hipError_t launch_attend_kernel(const AttendParams& p, dim3 grid, hipStream_t st) {
     constexpr int W = attend_waves(RT, ROWS);
     constexpr int kRow = (D < 128 ? D : 128) + 4;
-    constexpr int slots = 4 * W * (kAttendSlots * Slot<D, GS>::kWords + 64 * RT) + (kQInLds<D, GS> ? 32 * W * D : 0);
+    constexpr int slots = 4 * W * (kAttendSlots * Slot<D, GS>::kWords + 64 * RT) + (kQInLds<D, GS> ? 32 * W * D : 0) +
+                          (WINDOW ? 4 * W * 16 * RT : 0);
     constexpr int sums = 4 * W * (16 * kRow + RT * 16 * 2);
     constexpr int bytes = slots > sums ? slots : sums;
     if constexpr (bytes > 64 * 1024) {
         static std::atomic<uint64_t> raised{0};
         const hipError_t e =
-            raise_lds_limit(reinterpret_cast<const void*>(&attend_kernel<DT, D, GS, RT, ROWS, NT_LOADS>), raised);
+            raise_lds_limit(reinterpret_cast<const void*>(&attend_kernel<DT, D, GS, RT, ROWS, NT_LOADS, WINDOW>), raised);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((attend_kernel<DT, D, GS, RT, ROWS, NT_LOADS>), grid, dim3(64 * W), bytes, st, p);
+    hipLaunchKernelGGL((attend_kernel<DT, D, GS, RT, ROWS, NT_LOADS, WINDOW>), grid, dim3(64 * W), bytes, st, p);
     return hipGetLastError();
 }
 
@@ -1399,37 +1487,37 @@ hipError_t launch_attend_kernel(const AttendParams& p, dim3 grid, hipStream_t st
 // four row groups, 4096 tokens: 64 sequences of 4 heads 195 us, streamed 216, 16
 // of 8 heads 84 and 96; of 64 sequences of 8 heads, 604 MB, 448 and 422.  Heads
 // of 128, eight row groups over 16k: either way 120.
-template <int DT, int D, int GS>
+template <int DT, int D, int GS, bool WINDOW>
 hipError_t run_attend(const AttendParams& p, int row_tiles, bool by_rows, dim3 grid, hipStream_t st) {
     if constexpr (D <= 128) {
-        if (row_tiles == 2 && by_rows) return launch_attend_kernel<DT, D, GS, 2, true, false>(p, grid, st);
-        if (row_tiles == 2 && grid.y > 1) return launch_attend_kernel<DT, D, GS, 2, false, false>(p, grid, st);
-        if (row_tiles == 2) return launch_attend_kernel<DT, D, GS, 2, false, true>(p, grid, st);
+        if (row_tiles == 2 && by_rows) return launch_attend_kernel<DT, D, GS, 2, true, false, WINDOW>(p, grid, st);
+        if (row_tiles == 2 && grid.y > 1) return launch_attend_kernel<DT, D, GS, 2, false, false, WINDOW>(p, grid, st);
+        if (row_tiles == 2) return launch_attend_kernel<DT, D, GS, 2, false, true, WINDOW>(p, grid, st);
     }
-    if (by_rows) return launch_attend_kernel<DT, D, GS, 1, true, false>(p, grid, st);
+    if (by_rows) return launch_attend_kernel<DT, D, GS, 1, true, false, WINDOW>(p, grid, st);
     if constexpr (D == 256)
-        if (grid.y > 1) return launch_attend_kernel<DT, D, GS, 1, false, false>(p, grid, st);
-    return launch_attend_kernel<DT, D, GS, 1, false, true>(p, grid, st);
+        if (grid.y > 1) return launch_attend_kernel<DT, D, GS, 1, false, false, WINDOW>(p, grid, st);
+    return launch_attend_kernel<DT, D, GS, 1, false, true, WINDOW>(p, grid, st);
 }
 
-// One translation unit per type and head size.
+// One translation unit per type and head size, with a window and without.
 using AttendFn = hipError_t (*)(const AttendParams&, int row_tiles, bool by_rows, dim3, hipStream_t);
-template <int DT, int D>
+template <int DT, int D, bool WINDOW>
 AttendFn attend_fn(int gs);
 
 }  // namespace kv
 }  // namespace qmm
 
-#define QMM_KV_ATTEND_UNIT(DTV, DV)                             \
-    namespace qmm {                                             \
-    namespace kv {                                              \
-    template <>                                                 \
-    AttendFn attend_fn<DTV, DV>(int gs) {                       \
-        if (gs == 32) return run_attend<DTV, DV, 32>;           \
-        if (gs == 64) return run_attend<DTV, DV, 64>;           \
-        if constexpr (DV >= 128)                                \
-            if (gs == 128) return run_attend<DTV, DV, 128>;     \
-        return nullptr;                                         \
-    }                                                           \
-    }                                                           \
+#define QMM_KV_ATTEND_UNIT(DTV, DV, WINDOWV)                           \
+    namespace qmm {                                                    \
+    namespace kv {                                                     \
+    template <>                                                        \
+    AttendFn attend_fn<DTV, DV, WINDOWV>(int gs) {                     \
+        if (gs == 32) return run_attend<DTV, DV, 32, WINDOWV>;         \
+        if (gs == 64) return run_attend<DTV, DV, 64, WINDOWV>;         \
+        if constexpr (DV >= 128)                                       \
+            if (gs == 128) return run_attend<DTV, DV, 128, WINDOWV>;   \
+        return nullptr;                                                \
+    }                                                                  \
+    }                                                                  \
     }

@@ -197,9 +197,12 @@ class KVCache:
         _check(_lib.qmm_kv_read(*args, k.data_ptr(), v.data_ptr(), self._raw(stream)), "qmm_kv_read")
         return k, v
 
-    def attend_workspace_bytes(self, seqs: int, max_new: int, rows: int, heads: int, max_len: int) -> int:
+    def attend_workspace_bytes(self, seqs: int, max_new: int, rows: int, heads: int, max_len: int,
+                               window: int | None = None, sinks: int = 0) -> int:
         """Bytes of workspace :meth:`attend` needs (0: none)."""
-        n = int(_lib.qmm_kv_attend_workspace_bytes(self._c, seqs, max_new, rows, heads, max_len))
+        sizes = (self._c, seqs, max_new, rows, heads, max_len)
+        n = int(_lib.qmm_kv_attend_workspace_bytes(*sizes) if window is None else
+                _lib.qmm_kv_attend_window_workspace_bytes(*sizes, window, sinks))
         if n < 0:
             raise QmmError(n, "qmm_kv_attend_workspace_bytes")
         return n
@@ -207,12 +210,15 @@ class KVCache:
     def attend(self, layer: int, q: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor,
                starts: torch.Tensor | None = None, max_new: int | None = None, mask: torch.Tensor | None = None,
                scale: float | None = None, max_len: int | None = None, out: torch.Tensor | None = None,
-               lse: bool | torch.Tensor = False, workspace: torch.Tensor | None = None, stream=None):
+               lse: bool | torch.Tensor = False, workspace: torch.Tensor | None = None, stream=None,
+               window: int | None = None, sinks: int = 0):
         """Attention of the new tokens' q [rows, heads, head_dim] over ``layer``: out [rows, heads, head_dim].
 
         A row sees all tokens before its sequence's new ones and of these the
         ones up to itself, or with ``mask`` (int64 [rows]) the new tokens j
         whose bit j its word has set.  A row that sees nothing gives zeros.
+        With ``window``, of those tokens the last ``window`` and the ones at
+        positions below ``sinks``; pages of other tokens are not read.
         ``scale`` defaults to 1/sqrt(head_dim).  ``max_len`` bounds the
         lengths for the split of the work (default: what the tables hold).
         ``workspace``: from :meth:`attend_workspace` (default: one that the
@@ -240,17 +246,26 @@ class KVCache:
             _same_device(q, (mask, "mask"))
         if max_len is None:
             max_len = max(1, args[6] * self.page_size)
+        if window is None:
+            if sinks:
+                raise ValueError("sinks need a window")
+            seen = ()
+        elif window < 1 or sinks < 0:
+            raise ValueError(f"window={window} and sinks={sinks}: at least 1 and 0")
+        else:
+            seen = (window, sinks)
         raw = self._raw(stream)
         if workspace is None:
-            workspace, nbytes = self._own_space(stream, raw, args[2], args[3], rows, heads, max_len)
+            workspace, nbytes = self._own_space(stream, raw, args[2], args[3], rows, heads, max_len, *seen)
         else:
             _dev(workspace, "workspace")
             _same_device(q, (workspace, "workspace"))
             nbytes = workspace.numel() * workspace.element_size()
-        _check(_lib.qmm_kv_attend(*args, ptr, qr, qh, heads, self._scale if scale is None else scale,
-                                  None if mask is None else mask.data_ptr(), out.data_ptr(),
-                                  None if lse is False else lse.data_ptr(), max_len,
-                                  None if workspace is None else workspace.data_ptr(), nbytes, raw), "qmm_kv_attend")
+        _check((_lib.qmm_kv_attend_window if seen else _lib.qmm_kv_attend)(
+            *args, ptr, qr, qh, heads, self._scale if scale is None else scale, None if mask is None else mask.data_ptr(), *seen,
+            out.data_ptr(), None if lse is False else lse.data_ptr(), max_len,
+            None if workspace is None else workspace.data_ptr(), nbytes, raw),
+            "qmm_kv_attend_window" if seen else "qmm_kv_attend")
         return out if lse is False else (out, lse)
 
     # ---- pages ----

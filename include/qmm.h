@@ -459,6 +459,27 @@ int qmm_kv_attend(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t ma
                   void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
+ * Attention with a window and sinks: as qmm_kv_attend, but of the tokens that
+ * a row would see there, in order of their positions, it sees the last
+ * `window` (1 or more) and besides those at positions below `sinks` (0 or
+ * more).  A row of a draft tree thus has its own token, its ancestors and as
+ * many tokens before the new ones as fill the window.  Tokens count whether
+ * or not a page holds them.  Reads the pages of those tokens and no others:
+ * table entries of pages that no row sees may be negative.
+ * The workspace is qmm_kv_attend's, at least
+ * qmm_kv_attend_window_workspace_bytes(...) bytes (the same bound and
+ * QMM_KV_ATTEND_ZEROED_BYTES hold; one workspace may serve both calls in
+ * turn).  window < 1 or sinks < 0 -> QMM_ERR_INVALID_ARG.
+ */
+int64_t qmm_kv_attend_window_workspace_bytes(const qmm_kv_cache* cache, int64_t seqs, int64_t max_new, int64_t rows,
+                                             int64_t heads, int64_t max_len, int64_t window, int64_t sinks);
+int qmm_kv_attend_window(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t max_new, int64_t rows,
+                         const int32_t* tables, int64_t table_width, const int32_t* lens, const int32_t* starts,
+                         const void* q, int64_t q_stride_row, int64_t q_stride_head, int64_t heads, float scale,
+                         const int64_t* mask, int64_t window, int64_t sinks, void* out, float* lse, int64_t max_len,
+                         void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
  * Pages.  All layers move together; ids out of range are skipped.
  *
  * qmm_kv_copy_pages: page dst[i] <- page src[i] for i < n (device int32
@@ -508,6 +529,121 @@ int qmm_kv_free(const qmm_kv_cache* cache, int64_t seqs, int32_t* tables, int64_
 int qmm_kv_compact(const qmm_kv_cache* cache, int64_t seqs, const int32_t* tables, int64_t table_width,
                    const int32_t* refs, int32_t* tables_out, int32_t* refs_out, int32_t* live_out, void* workspace,
                    int64_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * What lies between the products and the cache in a decoder's step: the gated
+ * block, rotary positions, log probabilities.  Arrays and types as above
+ * unless said; every call may be captured in a graph.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Gated block: h [M, F] = act(x . Wg^T) * (x . Wu^T) with W = [Wg; Wu]
+ * (dequantized) of wq [2F, K*bits/32], scales, biases [2F, K/gs]: the gate's
+ * rows first, as one qmm_quantize of both leaves them.  Both products,
+ * accumulated in fp32, go through the activation in fp32; h is rounded once.
+ * K obeys qmm_small_m's rules, F is any; 1 <= M <= 64.  Deterministic.
+ * Statuses as qmm_small_m (M == 0 or F == 0: QMM_OK, nothing launched); an
+ * unknown act -> QMM_ERR_UNSUPPORTED.
+ */
+enum qmm_act {
+    QMM_ACT_SILU = 0,
+    QMM_ACT_GELU = 1,       /* a Phi(a), by the error function */
+    QMM_ACT_GELU_TANH = 2,  /* its form by tanh */
+    QMM_ACT_RELU = 3        /* slope 0 at 0 */
+};
+int qmm_gated(int dt, int bits, int group_size, int act, int64_t M, int64_t F, int64_t K, const void* x,
+              const uint32_t* wq, const void* scales, const void* biases, void* h, void* stream);
+
+/*
+ * Its gradient for given (constant) weights: with g, u the two products, formed
+ * again, and grad [M, F] that of h,
+ *   grad_gate_up [M, 2F] = [grad * u * act'(g), grad * act(g)]
+ *   grad_x [M, K]        = grad_gate_up . W
+ * grad_gate_up is rounded once to dt; grad_x is formed from its fp32 values,
+ * kept to 16 bits, and rounded once.  F a multiple of 16 (QMM_ERR_UNSUPPORTED
+ * otherwise).
+ * workspace: device memory of at least qmm_gated_backward_workspace_bytes(...)
+ * bytes (a negative status for what is not supported), 16-byte aligned, not
+ * aliasing the other arrays; two calls in flight need two.
+ */
+int64_t qmm_gated_backward_workspace_bytes(int dt, int bits, int group_size, int64_t M, int64_t F, int64_t K);
+int qmm_gated_backward(int dt, int bits, int group_size, int act, int64_t M, int64_t F, int64_t K, const void* x,
+                       const uint32_t* wq, const void* scales, const void* biases, const void* grad,
+                       void* grad_gate_up, void* grad_x, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Rotary positions: out = x [rows][heads][head_dim] with the pairs p <
+ * rotary_dim / 2 of every head of row r turned by positions[axis(p)][r] *
+ * freq[p]:
+ *   (a, b) -> (scale * (a cos - b sin), scale * (b cos + a sin)),
+ * by minus the angle with inverse != 0 (which is the gradient's map); values
+ * behind rotary_dim stay as they are.  A pair is (p, p + rotary_dim / 2)
+ * with QMM_PAIRS_HALVES, (2p, 2p + 1) with QMM_PAIRS_ADJACENT.
+ *   - axes 1..4; sections (host, [axes]; may be NULL with one axis) are the
+ *     numbers of consecutive pairs of each axis, rotary_dim / 2 together.
+ *   - positions: int32, or int64 with positions_64 != 0, [axes][rows], the
+ *     axes position_stride elements apart; any values (angles are formed in
+ *     fp64, to 2^-51 of themselves).  freq: fp32 [rotary_dim / 2], radians.
+ *   - head_dim a multiple of 8 up to 1024, rotary_dim a multiple of 16 up to
+ *     head_dim (QMM_ERR_UNSUPPORTED otherwise).
+ *   - x, out: element (row, head, d) at row * stride_row + head * stride_head
+ *     + d; bases 16-byte aligned, strides (elements, >= 0) multiples of 8.
+ *     out may be x with the same strides; no two places of out may overlap
+ *     (QMM_ERR_INVALID_ARG).
+ */
+enum qmm_pairs { QMM_PAIRS_HALVES = 0, QMM_PAIRS_ADJACENT = 1 };
+int qmm_rotary(int dt, int64_t rows, int64_t heads, int64_t head_dim, int64_t rotary_dim, int pairs, int inverse,
+               float scale, const void* x, int64_t x_stride_row, int64_t x_stride_head, const void* positions,
+               int positions_64, int64_t position_stride, int axes, const int32_t* sections, const float* freq,
+               void* out, int64_t out_stride_row, int64_t out_stride_head, void* stream);
+
+/*
+ * Log probabilities of rows of logits [rows][vocab] (dt; row r at r * stride
+ * elements, stride >= 0, any alignment of 2 bytes), z = scale * logit, scale
+ * finite and above 0 (QMM_ERR_INVALID_ARG otherwise):
+ *   lse [rows]                 ln sum_v exp z_v
+ *   entropy [rows]             -sum_v p_v ln p_v (nats), p_v = exp(z_v - lse)
+ *   token_logprobs [rows][given]  z_t - lse of tokens [rows][given] (int32, or
+ *                              int64 with tokens_64 != 0); 0 where t lies
+ *                              outside 0..vocab-1 (padding)
+ *   top_logprobs, top_ids [rows][top]  the `top` likeliest, likeliest first,
+ *                              of equal logits the lowest id
+ * all fp32, ids int64.  given 0..64 and top 0..min(64, vocab)
+ * (QMM_ERR_UNSUPPORTED otherwise; arrays of none may be NULL).
+ * Logits may be -infinity (barred): probability 0, log probability -infinity.
+ * A row of nothing else has lse and log probabilities -infinity and entropy
+ * 0.  A row with NaN or +infinity has NaN for all and ids of -1.  |z| of
+ * finite logits is to stay below 2^127.
+ * Deterministic.
+ * workspace: QMM_LOG_PROBS_WORKSPACE_BYTES of device memory, 16-byte aligned,
+ * whose first QMM_LOG_PROBS_ZEROED_BYTES are zero before the first call that
+ * uses it; every call leaves them zero (calls of any sizes may follow each
+ * other on one workspace, two in flight need two).  It may be NULL where
+ * qmm_log_probs_needs_workspace(rows, vocab) is 0 (1: needed, or a negative
+ * status).
+ */
+#define QMM_LOG_PROBS_MOST_TOP 64
+#define QMM_LOG_PROBS_ZEROED_BYTES 65536
+#define QMM_LOG_PROBS_WORKSPACE_BYTES (65536 + 1024 * 66 * 8)
+int qmm_log_probs_needs_workspace(int64_t rows, int64_t vocab);
+int qmm_log_probs(int dt, int64_t rows, int64_t vocab, float scale, const void* logits, int64_t stride,
+                  const void* tokens, int tokens_64, int64_t given, int64_t top, float* lse, float* entropy,
+                  float* token_logprobs, float* top_logprobs, int64_t* top_ids, void* workspace,
+                  int64_t workspace_bytes, void* stream);
+
+/*
+ * Its gradient, with lse and entropy as qmm_log_probs left them: of
+ *   sum grad_tokens * token_logprobs + grad_entropy * entropy + grad_lse * lse
+ * for the logits, out [rows][vocab] (dt, rounded once; row r at r * out_stride
+ * elements, out_stride >= vocab).  Each of the three may be NULL (entropy too
+ * without grad_entropy).  A token named twice counts twice; padding has no
+ * part.  Rows whose lse is -infinity get zeros.  out may be logits with the
+ * same stride.
+ */
+int qmm_log_probs_backward(int dt, int64_t rows, int64_t vocab, float scale, const void* logits, int64_t stride,
+                           const void* tokens, int tokens_64, int64_t given, const float* lse, const float* entropy,
+                           const float* grad_tokens, const float* grad_entropy, const float* grad_lse, void* out,
+                           int64_t out_stride, void* stream);
 
 #ifdef __cplusplus
 }

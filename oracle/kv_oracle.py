@@ -105,7 +105,18 @@ def read(c, layer, tables, lens, starts, kv_heads):
     return out[0], out[1]
 
 
-def attend(c, layer, q, tables, lens, starts, scale, mask=None):
+def sees(word, positions, length, n, window=None, sinks=0):
+    """Which of the positions a row sees: all before the sequence's n new ones, and of these the ones in its word; with a
+    window the last `window` of those, and the ones below `sinks`."""
+    before = length - n
+    if window is None:
+        return np.array([t < before or (t - before < 64 and word >> (t - before) & 1) for t in positions], dtype=bool)
+    seen = [t for t in range(max(length, 0)) if t < before or (t - before < 64 and word >> (t - before) & 1)]
+    seen = set(seen[-window:]) | {t for t in seen if t < sinks}
+    return np.array([t in seen for t in positions], dtype=bool)
+
+
+def attend(c, layer, q, tables, lens, starts, scale, mask=None, window=None, sinks=0):
     """q [rows, heads, dim] fp64 -> out, lse, and per element a coarse bound of how far a kernel may be off.
 
     The bound is that of a plainer kernel, which rounds more, and over many
@@ -142,9 +153,8 @@ def attend(c, layer, q, tables, lens, starts, scale, mask=None):
             vs, vz, vc = (np.array([d[j] for d in data[1]]).reshape(len(got), dim) for j in (1, 2, 0))
             kk, vv = ks * kc + kz, vs * vc + vz
             for i in range(n):
-                new = np.array(got, dtype=np.int64) - (int(lens[b]) - n)
                 word = int(mask[row + i]) if mask is not None else (2 << i) - 1
-                see = np.array([j < 0 or (j < 64 and word >> int(j) & 1) for j in new], dtype=bool)
+                see = sees(word, got, int(lens[b]), n, window, sinks)
                 if not see.any():
                     continue
                 for x in range(h * (heads // hk), (h + 1) * (heads // hk)):
@@ -167,7 +177,7 @@ def attend(c, layer, q, tables, lens, starts, scale, mask=None):
     return out, lse, tol, ltol
 
 
-def attend_bound(c, layer, q, tables, lens, starts, scale, mask=None):
+def attend_bound(c, layer, q, tables, lens, starts, scale, mask=None, window=None, sinks=0):
     """As ``attend``, with a bound that follows the kernel rounding by rounding: out, lse, tol, ltol.
 
     With weights w_t = p_t / l of the tokens that a row sees, p <= 1, out = sum w (s (code - 7.5) + m), m = b + 7.5 s.
@@ -201,7 +211,6 @@ def attend_bound(c, layer, q, tables, lens, starts, scale, mask=None):
         length = min(max(int(lens[b]), 0), cap)
         pages = [page_of(c, tables, b, t) for t in range(length)]
         got = [t for t in range(length) if pages[t] >= 0]
-        new = np.array(got, dtype=np.int64) - (int(lens[b]) - n)
         for h in range(hk if n else 0):
             data = [[load(c, layer, pages[t], h, t % c["page"], part) for t in got] for part in (0, 1)]
             kc, ks, kb, vc, vs, vb = (np.array([d[j] for d in data[i]]).reshape(len(got), dim)
@@ -209,7 +218,7 @@ def attend_bound(c, layer, q, tables, lens, starts, scale, mask=None):
             kk, vv = ks * kc + kb, vs * vc + vb
             for i in range(n):
                 word = int(mask[row + i]) if mask is not None else (2 << i) - 1
-                see = np.array([j < 0 or (j < 64 and word >> int(j) & 1) for j in new], dtype=bool)
+                see = sees(word, got, int(lens[b]), n, window, sinks)
                 if not see.any():
                     continue
                 s, v, m, off = vs[see], vv[see], vb[see] + 7.5 * vs[see], np.abs(vc[see] - 7.5)
