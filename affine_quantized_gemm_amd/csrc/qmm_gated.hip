@@ -36,29 +36,42 @@ hipError_t launch_gated(const GatedArgs& a) {
     p.K = a.K;
     p.words = static_cast<int>(a.K * a.bits / 32);
     p.groups = static_cast<int>(a.K / a.gs);
-    p.supers = static_cast<int>((a.K + kSuper - 1) / kSuper);
-    const bool vec = a.K % kSuper == 0;
+    const int super = super_of(a.bits);
+    p.supers = static_cast<int>((a.K + super - 1) / super);
+    const bool vec = a.K % super == 0;
     const int rt = !vec || a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
     const int row_blocks = static_cast<int>((a.M + 16 * rt - 1) / (16 * rt));
     const int rows = static_cast<int>(a.M < 16 * rt ? a.M : 16 * rt);
     const int64_t tiles16 = (a.F + 15) / 16;
-    // shares of K until the wavefronts fill the chip; x of all shares goes through LDS together
-    const int most = kChunkBytes / (2 * rows * kSuper);  // superblocks of x in LDS
-    const int64_t fill = rt <= 2 ? 4096 : 2048;
-    while ((2 << p.ks_shift) <= kWaves && (2 << p.ks_shift) <= most && (1 << p.ks_shift) < p.supers &&
-           (tiles16 << p.ks_shift) * row_blocks < fill)
+    // the wavefronts that all superblocks would keep busy, one each, are few
+    const bool few = rt == 1 && tiles16 * row_blocks * (p.supers < 16 ? p.supers : 16) <= 128 * 16;
+    const int waves = waves_of(rt, few);
+    // superblocks of x that LDS holds beside the slots
+    int most = (kLds - waves * slot_bytes(a.bits, a.gs, rt) - 16 * rows) / (2 * super * rows + 4 * (super / a.gs) * sums_of(rt));
+    int held = 64 * waves * 8 / super;  // a row's pieces are at most the threads
+    if (rt > 1) {                       // and a chunk passes through their registers
+        const int all = pieces_of(rt) * 64 * waves * 8 / (rows * super);
+        held = all < held ? all : held;
+    }
+    most = held < most ? held : most;
+    // shares of K (x of all of them goes through LDS together) for as many workgroups as the chip holds at a time
+    const int64_t hold = 256;
+    while ((2 << p.ks_shift) <= waves && (2 << p.ks_shift) <= most && (1 << p.ks_shift) < p.supers &&
+           (tiles16 << (p.ks_shift + 1)) * row_blocks <= hold * waves)
         ++p.ks_shift;
     const int ks = 1 << p.ks_shift;
-    const int whole = (p.supers + ks - 1) / ks * ks, part = most / ks * ks;
-    p.chunk = kSuper * (whole < part ? whole : part);
-    p.chunks = (p.supers * kSuper + p.chunk - 1) / p.chunk;
-    const int64_t tiles = (tiles16 * ks + kWaves - 1) / kWaves;
+    const int64_t tiles = (tiles16 * ks + waves - 1) / waves;
     if (tiles > INT32_MAX / 2) return hipErrorInvalidValue;
     p.tiles = static_cast<int>(tiles);
-    // workgroups that the chip holds at a time; a multiple of 8, so that the row blocks of a column share an XCD's L2
-    const int64_t hold = 512;
+    // a multiple of 8, so that the row blocks of a column share an XCD's L2
     const int64_t grid_x = tiles < hold ? (tiles + 7) / 8 * 8 : hold;
-    const int bytes = lds_bytes(rows, p.chunk, p.chunks, a.gs, rt);
+    p.per = (p.supers + ks - 1) / ks;
+    if (tiles > grid_x) p.per += p.per % 2;
+    while ((1 << p.steps_shift) < p.per && (2 << p.steps_shift) * ks <= most) ++p.steps_shift;
+    p.chunk = super * ks << p.steps_shift;
+    p.piece_shift = __builtin_ctz(p.chunk / 8);
+    p.chunks = (p.per + (1 << p.steps_shift) - 1) >> p.steps_shift;
+    const int bytes = lds_bytes(a.bits, a.gs, rt, waves, rows, p.chunk);
     const dim3 grid(static_cast<unsigned>(grid_x), static_cast<unsigned>(row_blocks));
     GatedFn fn = nullptr;
     const bool half = a.dt == DT_F16;
@@ -68,7 +81,7 @@ hipError_t launch_gated(const GatedArgs& a) {
         case 8: fn = half ? gated_fn<DT_F16, 8>(a.gs) : gated_fn<DT_BF16, 8>(a.gs); break;
         default: break;
     }
-    return fn != nullptr ? fn(p, rt, vec, grid, bytes, a.stream) : hipErrorInvalidValue;
+    return fn != nullptr ? fn(p, rt, few, vec, grid, bytes, a.stream) : hipErrorInvalidValue;
 }
 
 // Slices for the workgroups that the chip holds at a time: two a CU with one

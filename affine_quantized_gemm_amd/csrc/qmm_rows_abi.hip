@@ -30,7 +30,8 @@ int check_gated(int dt, int bits, int gs, int64_t M, int64_t F, int64_t K) {
     if (bits != 4 && bits != 6 && bits != 8) return QMM_ERR_UNSUPPORTED;
     if (gs != 32 && gs != 64 && gs != 128) return QMM_ERR_UNSUPPORTED;
     if (K < 64 || K % 64 != 0 || K % gs != 0) return QMM_ERR_UNSUPPORTED;
-    if (F > INT32_MAX / 2 || K > INT32_MAX / 8 || M > 64) return QMM_ERR_UNSUPPORTED;
+    // (offsets within x and within 16 rows of weights are 32-bit)
+    if (F > INT32_MAX / 2 || K > (1 << 24) || M > 64) return QMM_ERR_UNSUPPORTED;
     return QMM_OK;
 }
 

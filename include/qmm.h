@@ -541,7 +541,7 @@ int qmm_kv_compact(const qmm_kv_cache* cache, int64_t seqs, const int32_t* table
  * (dequantized) of wq [2F, K*bits/32], scales, biases [2F, K/gs]: the gate's
  * rows first, as one qmm_quantize of both leaves them.  Both products,
  * accumulated in fp32, go through the activation in fp32; h is rounded once.
- * K obeys qmm_small_m's rules, F is any; 1 <= M <= 64.  Deterministic.
+ * K obeys qmm_small_m's rules, up to 2^24, F is any; 1 <= M <= 64.  Deterministic.
  * Statuses as qmm_small_m (M == 0 or F == 0: QMM_OK, nothing launched); an
  * unknown act -> QMM_ERR_UNSUPPORTED.
  */
