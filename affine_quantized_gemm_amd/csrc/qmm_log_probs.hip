@@ -12,10 +12,17 @@
 // The likeliest tokens: a logit's 16 bits as an ordered number and its column
 // make a key without equals (of equal logits the lowest column is first), so
 // the selection is exact and has one answer.  A wavefront keeps the keys of
-// the `top` best of its columns in LDS; a slice of 1024 columns is looked at
-// closer only where a lane's largest passes the wavefront's last one.  Of
-// such a slice no more is collected than what is at or above the top-th of
-// the lanes' largest: at most 16 values of `top` lanes, whatever the values are.
+// the `top` best of its columns, one a lane; a slice of 1024 columns is looked
+// at closer only where a lane's largest passes the last one of the wavefront's
+// keys, that of another wavefront of the workgroup, and the least of the four
+// wavefronts' (top / 4)-th.  A few such lanes' values
+// are put in one by one (a comparison, a count of lanes and a shift by a lane).
+// Of a slice with many no more is collected, in LDS, than what is at or above
+// the top-th of the lanes' largest: at most 16 values of `top` lanes, whatever
+// the values are.  (1000 rows of 152k, fp16: none likeliest 64 us, 1 78, 5 96,
+// 20 112, 64 464.  The 20 took 163 us without the first way and the others'
+// keys, 128 without their (top / 4)-th.)  What bounds it is the vector units'
+// work a logit: the exponential, t's cut and the two sums, 64 us of it.
 //
 // A row is one workgroup's, or cut into parts of whole slices where rows are
 // few; the workgroup that is last to finish a row joins the parts.
@@ -44,6 +51,7 @@ constexpr int kDoneStride = 32;                 // counters in lines of their ow
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 constexpr float kFarBelow = -1e30f;
 constexpr int kNothing = -32768;                // below every ordered logit that is a number
+constexpr int kFewLanes = 6;                    // whose values are put in one by one
 
 // 64-bit words of a part: m and L, W, then its keys.
 constexpr int part_words(int top) { return 2 + top; }
@@ -71,11 +79,6 @@ template <int DT>
 __device__ __forceinline__ float ordered_f32(int o) {
     return DtOps<DT>::to_f32(static_cast<uint16_t>(o < 0 ? (o - 1) ^ 0x7FFF : o));
 }
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
-    typedef short short2_t __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(short2_t, a), __builtin_bit_cast(short2_t, b)));
-}
-
 // Over the wavefront, in every lane.
 template <class F>
 __device__ __forceinline__ uint32_t wave_reduce(uint32_t v, F f) {
@@ -161,16 +164,55 @@ __device__ __forceinline__ void lds_order() {
     __builtin_amdgcn_wave_barrier();
 }
 
+struct Piece {
+    uint32_t w[4];
+};
+// What lanes load where a row has no whole piece.
+__device__ const uint4 kNoPiece = {0, 0, 0, 0};
+// The largest of a lane's logits.
+template <int DT>
+__device__ __forceinline__ float largest(const Piece (&q)[kVecs]) {
+    if constexpr (DT == DT_F16) {
+        typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+        half2_t m = __builtin_bit_cast(half2_t, q[0].w[0]);
+#pragma unroll
+        for (int n = 0; n < kVecs; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m = __builtin_elementwise_max(m, __builtin_bit_cast(half2_t, q[n].w[e]));
+        return fmaxf(static_cast<float>(m[0]), static_cast<float>(m[1]));
+    } else {
+        float m = -__builtin_inff();
+#pragma unroll
+        for (int n = 0; n < kVecs; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(low_f32<DT>(q[n].w[e]), high_f32<DT>(q[n].w[e])));
+        return m;
+    }
+}
+
+// From the lane before (the first lane: 0).
+__device__ __forceinline__ uint32_t shift_lane(uint32_t v) {
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x138, 0xf, 0xf, false));
+}
+
 template <int DT, bool TOP>
 __global__ __launch_bounds__(kThreads) void log_probs_kernel(Params p) {
     extern __shared__ __align__(16) uint64_t lds[];
     __shared__ Sums joined[kWaves];
     __shared__ int counts[kWaves];
     __shared__ uint32_t last_flag;
+    // what `top` columns have been found at or above: the largest of the wavefronts' last keys' values, and the least of
+    // their ceil(top / 4)-th ones' (a third of the values that pass the former alone)
+    __shared__ int shared_least;
+    __shared__ __align__(16) int shared_part[kWaves];
+    if constexpr (TOP) {
+        if (threadIdx.x < kWaves) shared_part[threadIdx.x] = shared_least = kNothing;
+        __syncthreads();
+    }
     const LogProbsArgs& a = p.a;
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int top = a.top;
+    const int top = a.top, part_of = (top + kWaves - 1) / kWaves;
     const int64_t row = blockIdx.x / static_cast<uint32_t>(p.parts);
     const int part = blockIdx.x - static_cast<uint32_t>(row) * p.parts;
     const uint16_t* const z = static_cast<const uint16_t*>(a.logits) + row * a.stride;
@@ -189,18 +231,28 @@ __global__ __launch_bounds__(kThreads) void log_probs_kernel(Params p) {
     const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(z) & 15) / 2);
     const int64_t vecs = (a.vocab + shift + 7) / 8;
     const int64_t v_end = (part + 1) * p.part_vecs < vecs ? (part + 1) * p.part_vecs : vecs;
-    struct Piece {
-        uint32_t w[4];
-    };
-    auto load = [&](int64_t v) -> Piece {
-        Piece q;
-        const int64_t col = 8 * v - shift;
-        if (v < v_end && col >= 0 && col + 8 <= a.vocab) {
-            const mf::u32x4_t u = __builtin_nontemporal_load(reinterpret_cast<const mf::u32x4_t*>(z + col));
+    // Loads are issued for every slice, without a branch (one makes the waits for others wait for everything): of the
+    // row's nearest whole piece where a lane has none; those lanes' columns follow one by one when the slice is looked at.
+    const int64_t whole0 = shift > 0 ? 1 : 0, whole1 = (a.vocab + shift) / 8;  // whole pieces from, to
+    const bool tiny = whole1 <= whole0;
+    const uint16_t* const pieces = tiny ? reinterpret_cast<const uint16_t*>(&kNoPiece) : z - shift;
+    auto load = [&](Piece (&q)[kVecs], int64_t v0) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) q.w[e] = u[e];
-        } else {
-            // (columns outside the row are barred)
+        for (int n = 0; n < kVecs; ++n) {
+            int64_t v = v0 + 64 * n + lane;
+            v = v < whole1 ? v : whole1 - 1;
+            v = tiny ? 0 : v > whole0 ? v : whole0;
+            const mf::u32x4_t u = __builtin_nontemporal_load(reinterpret_cast<const mf::u32x4_t*>(pieces + 8 * v));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) q[n].w[e] = u[e];
+        }
+    };
+    auto mend = [&](Piece (&q)[kVecs], int64_t v0) {
+#pragma unroll
+        for (int n = 0; n < kVecs; ++n) {
+            const int64_t v = v0 + 64 * n + lane, col = 8 * v - shift;
+            if (v >= whole0 && v < whole1 && v < v_end) continue;
+            // (columns outside the row or the part are barred)
             constexpr uint32_t none = DT == DT_F16 ? 0xFC00u : 0xFF80u;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -210,39 +262,23 @@ __global__ __launch_bounds__(kThreads) void log_probs_kernel(Params p) {
                     const int64_t at = col + 2 * e + k;
                     h[k] = v < v_end && at >= 0 && at < a.vocab ? z[at] : none;
                 }
-                q.w[e] = h[0] | h[1] << 16;
+                q[n].w[e] = h[0] | h[1] << 16;
             }
         }
-        return q;
     };
 
     uint64_t* const keys = lds + wave * wave_keys(top);
-    int have = 0;             // kept keys, the best first
+    int have = 0;             // kept keys: lane i has the i-th best
+    uint64_t mine = 0;
     int least = kNothing - 1; // a later column has to be above it
     Sums s{-__builtin_inff(), 0.0f, 0.0f};
     int64_t v0 = part * p.part_vecs + static_cast<int64_t>(wave) * kSlice;
-    Piece q[kVecs];
-#pragma unroll
-    for (int n = 0; n < kVecs; ++n) q[n] = load(v0 + 64 * n + lane);
-    while (v0 < v_end) {
-        const int64_t next = v0 + kWaves * kSlice;
-        Piece ahead[kVecs];
-#pragma unroll
-        for (int n = 0; n < kVecs; ++n) ahead[n] = load(next + 64 * n + lane);
-        // the lane's largest, ordered
-        uint32_t o[kVecs][4], most2 = 0x80008000u;
-#pragma unroll
-        for (int n = 0; n < kVecs; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                o[n][e] = ordered2(q[n].w[e]);
-                most2 = max2(most2, o[n][e]);
-            }
-        const int hi = static_cast<int>(most2) >> 16, lo = static_cast<int16_t>(most2);
-        const int most = hi > lo ? hi : lo;
-        const float big = ordered_f32<DT>(most);
+    auto look = [&](Piece (&q)[kVecs]) {
+        const bool inner = v0 >= whole0 && v0 + kSlice <= whole1 && v0 + kSlice <= v_end;
+        if (!inner) mend(q, v0);
+        // the lane's largest (passes over NaN, which show in the sums)
+        const float big = largest<DT>(q);
         if (big > s.m) move(s, big, c);
-        else if (big != big) s.l = big;
         const float ref = reference(s.m);
 #pragma unroll
         for (int n = 0; n < kVecs; ++n)
@@ -258,74 +294,145 @@ __global__ __launch_bounds__(kThreads) void log_probs_kernel(Params p) {
                 }
             }
         if constexpr (TOP) {
-            const uint64_t over = __ballot(most > least);
+            // what a value has to pass: later columns the wavefront's own last key, any column the others' last value
+            int others = __hip_atomic_load(&shared_part[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) {
+                const int x = __hip_atomic_load(&shared_part[w], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+                others = x < others ? x : others;
+            }
+            const int most = __hip_atomic_load(&shared_least, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            others = __builtin_amdgcn_readfirstlane(most > others ? most : others);
+            const int pass = least >= others ? least : others - 1;
+            const uint64_t over = pass < kNothing ? ~uint64_t{0} : __ballot(big > ordered_f32<DT>(pass) || (pass == others - 1 && big >= ordered_f32<DT>(others)));
             if (over != 0) {
                 // the lane's keys within the slice: ordered logit, then columns from the last down; 0: not looked at
                 uint32_t own[kVecs][4][2], best = 0;
+                const int64_t first = 8 * v0 - shift;
 #pragma unroll
                 for (int n = 0; n < kVecs; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t o = ordered2(q[n].w[e]);
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const int x = k ? static_cast<int>(o[n][e]) >> 16 : static_cast<int16_t>(o[n][e]);
+                            const int x = k ? static_cast<int>(o) >> 16 : static_cast<int16_t>(o);
                             const int at = 512 * n + 8 * lane + 2 * e + k;
-                            const int64_t col = 8 * v0 - shift + at;
-                            const bool in = x > least && col >= 0 && col < a.vocab && v0 + 64 * n + lane < v_end;
+                            bool in = x > pass;
+                            if (!inner) in = in && first + at >= 0 && first + at < a.vocab && v0 + 64 * n + lane < v_end;
                             own[n][e][k] = in ? static_cast<uint32_t>(x + 32768) << 16 | (0xFFFFu - at) : 0;
                             best = own[n][e][k] > best ? own[n][e][k] : best;
                         }
-                // the top-th of the lanes' best
-                uint32_t from = 1;
-                if (__popcll(__ballot(best != 0)) > top) {
-                    int rank = 0;
-#pragma unroll 8
-                    for (int k = 0; k < 64; ++k) rank += static_cast<uint32_t>(__builtin_amdgcn_readlane(best, k)) > best;
-                    const uint64_t at = __ballot(rank == top - 1 && best != 0);
-                    from = __builtin_amdgcn_readlane(best, __builtin_ctzll(at));
-                }
-                int n_keys = have;
+                    }
+                const uint32_t columns = static_cast<uint32_t>(first);
+                auto whole = [&](uint32_t k) { return key_of(static_cast<int>(k >> 16) - 32768, columns + (0xFFFFu - (k & 0xFFFFu))); };
+                uint64_t some = __ballot(best != 0);
+                if (__popcll(some) <= kFewLanes) {
+                    while (some != 0) {
+                        const int l = __builtin_ctzll(some);
+                        const uint32_t k = __builtin_amdgcn_readlane(best, l);
+                        const uint64_t key = whole(k);
+                        // those before it stay, the others move on by a lane
+                        const bool before = mine > key;
+                        const uint32_t hi = shift_lane(static_cast<uint32_t>(mine >> 32)), lo = shift_lane(static_cast<uint32_t>(mine));
+                        const int place = __popcll(__ballot(before));
+                        if (!before) mine = lane == place ? key : static_cast<uint64_t>(hi) << 32 | lo;
+                        if (lane >= top) mine = 0;
+                        have = have < top ? have + 1 : top;
+                        best = 0;
 #pragma unroll
-                for (int n = 0; n < kVecs; ++n)
+                        for (int n = 0; n < kVecs; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
+                            for (int e = 0; e < 4; ++e)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const bool take = own[n][e][k] >= from;
-                            const uint64_t taken = __ballot(take);
-                            if (taken != 0) {
-                                if (take) {
-                                    const uint32_t col = static_cast<uint32_t>(8 * v0 - shift) + (0xFFFFu - (own[n][e][k] & 0xFFFFu));
-                                    keys[n_keys + __popcll(taken & ((uint64_t{1} << lane) - 1))] =
-                                        key_of(static_cast<int>(own[n][e][k] >> 16) - 32768, col);
+                                for (int h = 0; h < 2; ++h) {
+                                    own[n][e][h] = own[n][e][h] == k ? 0 : own[n][e][h];
+                                    best = own[n][e][h] > best ? own[n][e][h] : best;
                                 }
-                                n_keys += __popcll(taken);
+                        some = __ballot(best != 0);
+                    }
+                } else if (some != 0) {
+                    // the top-th of the lanes' best
+                    uint32_t from = 1;
+                    if (__popcll(some) <= top) {
+                    } else if (top <= 8) {
+                        from = ~0u;  // (a key is smaller: its column is below 1024)
+                        for (int k = 0; k < top; ++k) from = wave_max_u32(best < from ? best : 0);
+                        from = __builtin_amdgcn_readfirstlane(from);
+                    } else {
+                        int rank = 0;
+#pragma unroll 8
+                        for (int k = 0; k < 64; ++k) rank += static_cast<uint32_t>(__builtin_amdgcn_readlane(best, k)) > best;
+                        const uint64_t at = __ballot(rank == top - 1 && best != 0);
+                        from = __builtin_amdgcn_readlane(best, __builtin_ctzll(at));
+                    }
+                    if (lane < have) keys[lane] = mine;
+                    int n_keys = have;
+#pragma unroll
+                    for (int n = 0; n < kVecs; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const bool take = own[n][e][k] >= from;
+                                const uint64_t taken = __ballot(take);
+                                if (taken != 0) {
+                                    if (take) keys[n_keys + __popcll(taken & ((uint64_t{1} << lane) - 1))] = whole(own[n][e][k]);
+                                    n_keys += __popcll(taken);
+                                }
                             }
-                        }
-                lds_order();
-                // each key's place among them all; the first `top` stay
-                uint64_t* const fresh = keys + wave_keys(top) - top;
-                for (int k0 = 0; k0 < n_keys; k0 += 64) {
-                    const uint64_t key = k0 + lane < n_keys ? keys[k0 + lane] : 0;
-                    int place = 0;
-                    for (int k = 0; k < n_keys; ++k) place += keys[k] > key;
-                    if (k0 + lane < n_keys && place < top) fresh[place] = key;
+                    lds_order();
+                    // each key's place among them all; the first `top` stay
+                    uint64_t* const fresh = keys + wave_keys(top) - top;
+                    for (int k0 = 0; k0 < n_keys; k0 += 64) {
+                        const uint64_t key = k0 + lane < n_keys ? keys[k0 + lane] : 0;
+                        int place = 0;
+#pragma unroll 8
+                        for (int k = 0; k < n_keys; ++k) place += keys[k] > key;
+                        if (k0 + lane < n_keys && place < top) fresh[place] = key;
+                    }
+                    lds_order();
+                    have = n_keys < top ? n_keys : top;
+                    mine = lane < have ? fresh[lane] : 0;
+                    lds_order();
                 }
-                lds_order();
-                have = n_keys < top ? n_keys : top;
-                const uint64_t mine = lane < have ? fresh[lane] : 0;
-                if (lane < have) keys[lane] = mine;
-                if (have == top) least = static_cast<int>(__builtin_amdgcn_readlane(static_cast<uint32_t>(mine >> 32), top - 1)) - 32768;
-                lds_order();
+                if (have >= part_of) {
+                    const int part_least = static_cast<int>(__builtin_amdgcn_readlane(static_cast<uint32_t>(mine >> 32), part_of - 1)) - 32768;
+                    if (lane == 0) __hip_atomic_store(&shared_part[wave], part_least, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+                }
+                if (have == top) {
+                    least = static_cast<int>(__builtin_amdgcn_readlane(static_cast<uint32_t>(mine >> 32), top - 1)) - 32768;
+                    if (lane == 0) __hip_atomic_fetch_max(&shared_least, least, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+                }
             }
         }
+    };
+    // two slices on their way; one is taken out of its registers before the next is asked for
+    Piece even[kVecs], odd[kVecs];
+    load(even, v0);
+    load(odd, v0 + kWaves * kSlice);
+    auto turn = [&](Piece (&q)[kVecs]) {
+        Piece now[kVecs];
 #pragma unroll
-        for (int n = 0; n < kVecs; ++n) q[n] = ahead[n];
-        v0 = next;
+        for (int n = 0; n < kVecs; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                now[n].w[e] = q[n].w[e];
+                asm volatile("" : "+v"(now[n].w[e]));
+            }
+        load(q, v0 + 2 * kWaves * kSlice);
+        look(now);
+        v0 += kWaves * kSlice;
+    };
+    while (v0 < v_end) {
+        turn(even);
+        if (v0 >= v_end) break;
+        turn(odd);
     }
 
     // the wavefronts' sums and keys together
     s = wave_join(s, c);
+    if (TOP && lane < have) keys[lane] = mine;
     if (lane == 0) {
         joined[wave] = s;
         counts[wave] = have;
@@ -352,6 +459,7 @@ __global__ __launch_bounds__(kThreads) void log_probs_kernel(Params p) {
                 int place = n;  // (its own wavefront's are in order)
                 for (int u = 0; u < kWaves; ++u)
                     if (u != w)
+#pragma unroll 8
                         for (int k = 0; k < counts[u]; ++k) place += lds[u * wave_keys(top) + k] > key;
                 if (place < top) best[place] = key;
             }
