@@ -19,6 +19,7 @@ ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}  # qmm_act
 PAIRS = {"halves": 0, "adjacent": 1}                      # qmm_pairs
 LOG_PROBS_ZEROED_BYTES = 65536                            # QMM_LOG_PROBS_ZEROED_BYTES
 LOG_PROBS_WORKSPACE_BYTES = 65536 + 1024 * 66 * 8         # QMM_LOG_PROBS_WORKSPACE_BYTES
+_CODES, _GROUPS = (4, 6, 8), (32, 64, 128)
 _INTS = (torch.int32, torch.int64)
 
 
@@ -59,6 +60,12 @@ class _On:
             torch.cuda.ExternalStream(self.raw, device=self.device)
 
 
+def _fits(t, shape, dtype, index):
+    """Whether a GPU tensor is as expected; where one is not, the checks that name the fault are run (they take 1 to 2 us
+    an operand, this 0.4, and a small call's kernel runs 5)."""
+    return t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous()
+
+
 def _key(table, name, what):
     if name not in table:
         raise ValueError(f"{what} is {name!r}, expected one of {tuple(table)}")
@@ -84,6 +91,13 @@ def _check_gated(x, wq, scales, biases, bits, group_size):
     if wq.dim() != 2 or wq.shape[0] % 2:
         raise ValueError(f"wq must be 2-D [2F, K*bits/32], got shape {tuple(wq.shape)}")
     M, K = x.shape
+    # (what the library refuses of bits and group_size, it refuses itself)
+    if bits in _CODES and group_size in _GROUPS and K % group_size == 0:
+        rows, index = wq.shape[0], x.get_device()
+        groups = (rows, K // group_size)
+        if (index >= 0 and x.is_contiguous() and _fits(wq, (rows, K * bits // 32), torch.int32, index)
+                and _fits(scales, groups, x.dtype, index) and _fits(biases, groups, x.dtype, index)):
+            return dt, M, rows // 2, K
     _check_quantized(x.dtype, wq, scales, biases, wq.shape[0], K, bits, group_size)
     for t, n in ((x, "x"), (wq, "wq"), (scales, "scales"), (biases, "biases")):
         _dev(t, n)
@@ -162,7 +176,9 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, section
     if dim and x.stride(2) != 1:
         raise ValueError("x's last axis must be contiguous")
     axes = 1 if sections is None else len(sections)
-    if sections is None or (axes == 1 and positions.dim() == 1):
+    if _fits(positions, (rows,) if sections is None else (axes, rows), torch.int64, x.get_device()):
+        pass
+    elif sections is None or (axes == 1 and positions.dim() == 1):
         _expect(positions, "positions", (rows,), _INTS)
     else:
         _expect(positions, "positions", (axes, rows), _INTS)
@@ -170,9 +186,11 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, section
         raise ValueError("positions' last axis must be contiguous")
     if freq.dim() != 1:
         raise ValueError(f"freq must be 1-D [rotary_dim / 2], got shape {tuple(freq.shape)}")
-    _expect(freq, "freq", tuple(freq.shape), (torch.float32,))
-    _dev(freq, "freq")
-    _same_device(x, (positions, "positions"), (freq, "freq"))
+    if not _fits(freq, freq.shape, torch.float32, x.get_device()):
+        _expect(freq, "freq", tuple(freq.shape), (torch.float32,))
+        _dev(freq, "freq")
+        _same_device(x, (freq, "freq"))
+    _same_device(x, (positions, "positions"))
     if sections is None:
         cuts = None
     else:
@@ -256,9 +274,11 @@ def _check_logits(logits, tokens, scale):
         if tokens.dim() not in (1, 2):
             raise ValueError(f"tokens must be [rows] or [rows, n], got shape {tuple(tokens.shape)}")
         given = 1 if tokens.dim() == 1 else tokens.shape[1]
-        _expect(tokens, "tokens", (rows,) if tokens.dim() == 1 else (rows, given), _INTS)
-        _dev(tokens, "tokens")
-        _same_device(logits, (tokens, "tokens"))
+        shape = (rows,) if tokens.dim() == 1 else (rows, given)
+        if not _fits(tokens, shape, torch.int64, logits.get_device()):
+            _expect(tokens, "tokens", shape, _INTS)
+            _dev(tokens, "tokens")
+            _same_device(logits, (tokens, "tokens"))
     return dt, rows, vocab, logits.stride(0), given
 
 
@@ -275,7 +295,7 @@ def log_probs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top: int
     if not 0 <= top <= min(64, vocab):
         raise QmmError(QMM_ERR_UNSUPPORTED, f"top={top} of {vocab} tokens")
     with _On(logits, stream) as on:
-        sums = on.new((2, rows), torch.float32)
+        lse, entropy = on.new((rows,), torch.float32), on.new((rows,), torch.float32)
         lp = None if tokens is None else on.new(tuple(tokens.shape), torch.float32)
         values = ids = None
         if top:
@@ -285,16 +305,15 @@ def log_probs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top: int
             _same_device(logits, (workspace, "workspace"))
         elif _lib.qmm_log_probs_needs_workspace(rows, vocab) == 1:
             workspace = _own_space(on)
-        lse = sums.data_ptr()
         _check(_lib.qmm_log_probs(dt, rows, vocab, scale, logits.data_ptr(), stride,
                                   None if tokens is None else tokens.data_ptr(),
-                                  1 if tokens is not None and tokens.dtype is torch.int64 else 0, given, top, lse,
-                                  lse + 4 * rows, None if lp is None else lp.data_ptr(),
+                                  1 if tokens is not None and tokens.dtype is torch.int64 else 0, given, top, lse.data_ptr(),
+                                  entropy.data_ptr(), None if lp is None else lp.data_ptr(),
                                   None if values is None else values.data_ptr(), None if ids is None else ids.data_ptr(),
                                   None if workspace is None else workspace.data_ptr(),
                                   0 if workspace is None else workspace.numel() * workspace.element_size(), on.raw),
                "qmm_log_probs")
-    return LogProbs(sums[0], sums[1], lp, values, ids)
+    return LogProbs(lse, entropy, lp, values, ids)
 
 
 def log_probs_backward(logits: torch.Tensor, tokens: torch.Tensor | None, lse: torch.Tensor,
