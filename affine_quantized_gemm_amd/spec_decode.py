@@ -8,12 +8,14 @@ right now and then) continues one prompt in several ways at once:
   2. the other sequences fork from it and share its whole pages;
   3. every step drafts two branches of `depth` tokens each from the
      sequence's own history, verifies the tree of 1 + 2 * depth rows in one
-     pass (products of M = sequences * rows, append, attention under the
-     tree's mask), accepts the longer branch, and appends its keys and values
-     again, now in a row: what was rejected lies behind the length;
+     pass (products of M = sequences * rows, rotary positions, append,
+     attention under the tree's mask, gated blocks, the likeliest tokens with
+     their log probabilities), accepts the longer branch, and appends its keys
+     and values again, now in a row: what was rejected lies behind the length;
   4. half of the sequences end, their pages are freed and the rest compacted,
      and the others go on.
 
+With a window, the layers attend to the last tokens and the first few only.
 Nothing in a step waits for the device.  ``python -m
 affine_quantized_gemm_amd.spec_decode --help`` for the sizes.
 """
@@ -34,8 +36,9 @@ class Decoder:
     """Weights of a decoder with shared kv heads, gated MLP and rotary positions."""
 
     def __init__(self, layers=2, hidden=1024, heads=8, kv_heads=2, head_dim=128, ffn=2048, vocab=2048,
-                 dtype=torch.bfloat16, cycle=13, habit=7.0, seed=0):
+                 dtype=torch.bfloat16, cycle=13, habit=7.0, seed=0, window=None, sinks=0):
         self.layers, self.heads, self.kv_heads, self.head_dim, self.dtype = layers, heads, kv_heads, head_dim, dtype
+        self.window, self.sinks = window, sinks
         g = torch.Generator(device="cuda").manual_seed(seed)
         rand = lambda *shape: torch.randn(shape, generator=g, device="cuda")
         weight = lambda n, k: Q.quantize((rand(n, k) * k ** -0.5).to(dtype), BITS, GROUP)
@@ -61,25 +64,19 @@ class Decoder:
         f = x.float()
         return (f * torch.rsqrt(f.square().mean(-1, keepdim=True) + 1e-6)).to(self.dtype)
 
-    def _turn(self, x, cos, sin):
-        a, b = x.float().chunk(2, -1)
-        return torch.cat([a * cos - b * sin, b * cos + a * sin], -1).to(self.dtype)
-
     def forward(self, cache, tokens, positions, tables, lens, mask=None, max_len=None):
         """New tokens (at most 64, as many for each sequence) through all layers: logits, and every layer's k and v."""
         rows, H, kv = tokens.shape[0], self.heads, []
         x = self.embedding[tokens]
-        angle = positions[:, None, None] * self.freq
-        cos, sin = angle.cos(), angle.sin()
         for layer in range(self.layers):
             qkv = self._mul(self._norm(x), self.qkv[layer]).view(rows, H + 2 * self.kv_heads, self.head_dim)
-            turned, v = self._turn(qkv[:, :H + self.kv_heads], cos, sin), qkv[:, H + self.kv_heads:]
-            q, k = turned[:, :H], turned[:, H:]
+            q, k, v = qkv.split([H, self.kv_heads, self.kv_heads], 1)
+            turned = qkv[:, :H + self.kv_heads]
+            Q.rotary(turned, positions, self.freq, out=turned)  # q and k, in place
             cache.append(layer, k, v, tables, lens)
-            y = cache.attend(layer, q, tables, lens, mask=mask, max_len=max_len)
+            y = cache.attend(layer, q, tables, lens, mask=mask, max_len=max_len, window=self.window, sinks=self.sinks)
             x = x + self._mul(y.view(rows, -1), self.o[layer])
-            gate, up = self._mul(self._norm(x), self.gate_up[layer]).chunk(2, -1)
-            x = x + self._mul(torch.nn.functional.silu(gate) * up, self.down[layer])
+            x = x + self._mul(Q.gated(self._norm(x), *self.gate_up[layer], BITS, GROUP), self.down[layer])
             kv.append((k, v))
         return self._mul(self._norm(x), self.head), kv
 
@@ -93,6 +90,7 @@ class Sequences:
         self.model, self.cache, self.most = model, model.cache(seqs * width, page_size), width * page_size
         self.tables, self.lens, self.refs = int32(seqs, width) - 1, int32(seqs), int32(seqs * width)
         self.history = torch.zeros(seqs, most_tokens + 64, dtype=torch.int64, device="cuda")
+        self.said = torch.zeros(seqs, most_tokens + 64, device="cuda")     # the tokens' log probabilities (the first's is 0)
         self.tokens = torch.zeros(seqs, dtype=torch.int64, device="cuda")  # in the history; the last is not cached yet
         self.sound = torch.ones((), dtype=torch.int32, device="cuda")     # every page asked for was there
         # the draft tree: rows 0, 1..depth and depth + 1..2 * depth, what each sees, and its two paths
@@ -115,9 +113,11 @@ class Sequences:
             self._reserve(tables, lens, piece.numel())
             positions = torch.arange(at, at + piece.numel(), device="cuda")
             out.append(self.model.forward(self.cache, piece, positions, tables, lens, max_len=self.most)[0])
+        logits = torch.cat(out)
         self.history[0, :prompt.numel()] = prompt
+        self.said[0, 1:prompt.numel()] = Q.log_probs(logits[:-1], prompt[1:]).tokens
         self.tokens[0] = prompt.numel()
-        return torch.cat(out)
+        return logits
 
     def fork(self, logits: torch.Tensor) -> None:
         """All other sequences from sequence 0, each with another of the likeliest next tokens."""
@@ -127,7 +127,10 @@ class Sequences:
             ok = self.cache.fork(self.tables, self.lens, self.refs, torch.zeros_like(dst), dst)
             self.sound = torch.minimum(self.sound, ok.min())
         self.history[1:], self.tokens[1:] = self.history[0].clone(), self.tokens[0].clone()
-        self.history.scatter_(1, self.tokens[:, None], logits.float().topk(seqs).indices[:, None])
+        self.said[1:] = self.said[0].clone()
+        first = Q.log_probs(logits[None], top=seqs)
+        self.history.scatter_(1, self.tokens[:, None], first.top_ids.T)
+        self.said.scatter_(1, self.tokens[:, None], first.top_values.T)
         self.tokens += 1
 
     def _drafts(self):
@@ -148,7 +151,8 @@ class Sequences:
         positions = (start[:, None] + self.level).flatten()
         logits, kv = self.model.forward(self.cache, tree.flatten(), positions, self.tables, self.lens,
                                         self.sees.repeat(seqs), self.most)
-        picks = logits.view(seqs, R, -1).argmax(-1)
+        likeliest = Q.log_probs(logits, top=1)
+        picks, said = likeliest.top_ids.view(seqs, R), likeliest.top_values.view(seqs, R)
         # a draft is right if its parent's pick is that token
         right = [(tree[:, p[1:]] == picks[:, p[:-1]]).long().cumprod(1).sum(1) for p in self.paths]
         path, kept = self.paths[(right[1] > right[0]).long()], torch.maximum(*right)
@@ -158,7 +162,9 @@ class Sequences:
         for layer, (k, v) in enumerate(kv):
             self.cache.append(layer, k[rows], v[rows], self.tables, self.lens)
         self.lens.copy_(start + kept + 1)
-        self.history.scatter_(1, self.tokens[:, None] + torch.arange(self.depth + 1, device="cuda"), picks.gather(1, path))
+        places = self.tokens[:, None] + torch.arange(self.depth + 1, device="cuda")
+        self.history.scatter_(1, places, picks.gather(1, path))
+        self.said.scatter_(1, places, said.gather(1, path))
         self.tokens += kept + 1
 
     def end(self, which: list[int]) -> None:
@@ -167,12 +173,16 @@ class Sequences:
         self.tables, self.refs = self.cache.compact(self.tables, self.refs)[:2]
         keep = [i for i in range(self.lens.numel()) if i not in which]
         self.tables, self.lens = self.tables[keep].contiguous(), self.lens[keep]
-        self.history, self.tokens = self.history[keep], self.tokens[keep]
+        self.history, self.said, self.tokens = self.history[keep], self.said[keep], self.tokens[keep]
 
     def texts(self) -> list[list[int]]:
         """Every sequence's tokens so far."""
         assert int(self.sound) == 1, "the cache has too few pages"
         return [row[:n] for row, n in zip(self.history.tolist(), self.tokens.tolist())]
+
+    def scores(self) -> list[list[float]]:
+        """The log probability with which every one of those tokens came (the first's is 0)."""
+        return [row[:n] for row, n in zip(self.said.tolist(), self.tokens.tolist())]
 
 
 def logits_of(model: Decoder, tokens: list[int]) -> torch.Tensor:
@@ -193,11 +203,14 @@ def main(argv=None) -> None:
     p.add_argument("--kv-heads", type=int, default=8)
     p.add_argument("--ffn", type=int, default=14336)
     p.add_argument("--dtype", choices=["f16", "bf16"], default="bf16")
+    p.add_argument("--window", type=int, default=0, help="tokens that a row attends to (0: all)")
+    p.add_argument("--sinks", type=int, default=0, help="first tokens that it attends to besides")
     a = p.parse_args(argv)
     if a.seqs * (1 + 2 * a.depth) > 64:
         p.error("seqs * (1 + 2 * depth) rows: at most 64")
     model = Decoder(a.layers, a.hidden, a.heads, a.kv_heads, a.hidden // a.heads, a.ffn,
-                    dtype=torch.float16 if a.dtype == "f16" else torch.bfloat16)
+                    dtype=torch.float16 if a.dtype == "f16" else torch.bfloat16,
+                    window=a.window or None, sinks=a.sinks)
     s = Sequences(model, a.seqs, a.prompt + 1 + (2 * a.steps + 3) * (1 + 2 * a.depth), a.depth)
     prompt = torch.randint(0, model.embedding.shape[0], (a.prompt,), generator=torch.Generator().manual_seed(1)).cuda()
     s.fork(s.prefill(prompt)[-1])
@@ -214,8 +227,9 @@ def main(argv=None) -> None:
               f"{n / a.steps / seqs:.2f} tokens a step and sequence, {n / dt:.0f} tokens/s")
         if part == 0 and seqs > 1:
             s.end(list(range(seqs // 2, seqs)))
-    for text in s.texts():
-        print(f"  ... {text[a.prompt:a.prompt + 16]} ({len(text)} tokens)")
+    for text, said in zip(s.texts(), s.scores()):
+        said = said[a.prompt:]
+        print(f"  ... {text[a.prompt:a.prompt + 16]} ({len(text)} tokens, {sum(said) / len(said):.2f} nats each)")
 
 
 if __name__ == "__main__":

@@ -519,3 +519,37 @@ def test_a_step_on_another_stream(Q):
     h = Q.gated(x, *block("bf16", 4, 64, 6, 512, 256, 101)[2], 4, 64, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(r.top_ids, Q.log_probs(z, top=3).top_ids) and torch.equal(h, want[1])
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_decoding_with_a_window(Q, dt):
+    """The speculative decoder with a window and sinks in its layers: every token is the likeliest one of a plain pass over
+    its text, and came with that pass's log probability.
+
+    Both passes quantize keys and values that differ by roundings: the logits move by well under a tenth of their
+    deviation (a neighbouring code moves a score by 0.4 / sqrt(128), and as much of one token's share of the sums).  A
+    log probability, z - lse, moves by at most twice as much as the logits."""
+    from affine_quantized_gemm_amd import spec_decode as S
+    print(f"decoding with a window {dt}", flush=True)
+    model = S.Decoder(layers=2, hidden=512, heads=4, kv_heads=2, head_dim=128, ffn=512, vocab=512, dtype=DT[dt],
+                      window=48, sinks=4)
+    s = S.Sequences(model, 3, 70 + 1 + 45 * 7, 3)
+    prompt = torch.randint(0, 512, (70,), generator=torch.Generator().manual_seed(1)).cuda()
+    s.fork(s.prefill(prompt)[-1])
+    for _ in range(12):
+        s.step()
+    s.end([1])
+    for _ in range(8):
+        s.step()
+    for text, said in zip(s.texts(), s.scores()):
+        assert len(text) == len(said) > 71 + 20
+        logits = S.logits_of(model, text[:-1]).float()
+        far = 0.1 * logits.std(1)
+        got = logits.gather(1, torch.tensor(text[1:], device="cuda")[:, None])[:, 0]
+        assert (logits.amax(1) - got <= far)[70:].all()
+        off = (got - logits.logsumexp(1) - torch.tensor(said[1:], device="cuda")).abs()
+        assert (off <= 2 * far).all(), off.max()
+        # the window is one: without it the same text has other logits
+        whole = S.Decoder(layers=2, hidden=512, heads=4, kv_heads=2, head_dim=128, ffn=512, vocab=512, dtype=DT[dt])
+        assert torch.equal(S.logits_of(whole, text[:-1]).float()[:40], logits[:40])
+        assert not torch.equal(S.logits_of(whole, text[:-1]).float()[60:], logits[60:])
