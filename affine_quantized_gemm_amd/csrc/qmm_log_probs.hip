@@ -649,7 +649,7 @@ hipError_t launch_log_probs(int dt, const LogProbsArgs& a, hipStream_t st) {
     p.done = static_cast<uint32_t*>(a.workspace);
     p.sums = reinterpret_cast<uint64_t*>(static_cast<char*>(a.workspace) + QMM_LOG_PROBS_ZEROED_BYTES);
     const int64_t blocks = a.rows * p.parts;
-    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    if (blocks > UINT32_MAX / kThreads) return hipErrorInvalidValue;  // (a grid's threads are 32 bits)
     int64_t words = static_cast<int64_t>(kWaves) * wave_keys(a.top) + a.top;
     if (p.parts > 1 && words < static_cast<int64_t>(p.parts) * a.top) words = static_cast<int64_t>(p.parts) * a.top;
     const dim3 grid(static_cast<unsigned>(blocks));
@@ -667,7 +667,7 @@ hipError_t launch_log_probs(int dt, const LogProbsArgs& a, hipStream_t st) {
 hipError_t launch_log_probs_grad(int dt, const LogProbsGradArgs& a, hipStream_t st) {
     const int64_t vecs = (a.vocab + 7) / 8 + 1;
     const int64_t blocks_row = (vecs + kGradVecs * kThreads - 1) / (kGradVecs * kThreads);
-    if (blocks_row * a.rows > INT32_MAX) return hipErrorInvalidValue;
+    if (blocks_row * a.rows > UINT32_MAX / kThreads) return hipErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>(blocks_row * a.rows));
     if (dt == DT_F16)
         hipLaunchKernelGGL((log_probs_grad_kernel<DT_F16>), grid, dim3(kThreads), 0, st, a, static_cast<uint32_t>(blocks_row));

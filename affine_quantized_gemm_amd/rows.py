@@ -63,7 +63,7 @@ class _On:
 def _fits(t, shape, dtype, index):
     """Whether a GPU tensor is as expected; where one is not, the checks that name the fault are run (they take 1 to 2 us
     an operand, this 0.4, and a small call's kernel runs 5)."""
-    return t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous()
+    return isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous()
 
 
 def _key(table, name, what):
@@ -152,7 +152,8 @@ def gated_backward(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor, bias
                                        0 if workspace is None else workspace.numel() * workspace.element_size(), on.raw),
                "qmm_gated_backward")
         if F == 0:
-            out.zero_()
+            with torch.cuda.stream(on.torch_stream()):
+                out.zero_()
     return out, grad_gate_up
 
 

@@ -553,3 +553,17 @@ def test_decoding_with_a_window(Q, dt):
         whole = S.Decoder(layers=2, hidden=512, heads=4, kv_heads=2, head_dim=128, ffn=512, vocab=512, dtype=DT[dt])
         assert torch.equal(S.logits_of(whole, text[:-1]).float()[:40], logits[:40])
         assert not torch.equal(S.logits_of(whole, text[:-1]).float()[60:], logits[60:])
+
+
+def test_gradient_of_no_columns_on_a_stream(Q):
+    """A block without columns: grad_x is zero, in the order of the stream that was given."""
+    x = torch.ones(3, 64, dtype=torch.float16, device="cuda")
+    wq, s = torch.empty(0, 8, dtype=torch.int32, device="cuda"), torch.empty(0, 1, dtype=torch.float16, device="cuda")
+    out = torch.full_like(x, 7.0)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    dx, dgu = Q.gated_backward(x, wq, s, s.clone(), 4, 64, torch.empty(3, 0, dtype=torch.float16, device="cuda"), out=out, stream=stream)
+    with torch.cuda.stream(stream):
+        got = dx.clone()
+    stream.synchronize()
+    assert dx is out and dgu.shape == (3, 0) and not got.any()
