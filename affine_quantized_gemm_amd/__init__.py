@@ -185,6 +185,17 @@ def _stream(stream):
     return getattr(stream, "cuda_stream", stream)
 
 
+def _as_stream(stream, device):
+    """The torch stream of a call's ``stream``: one of torch's, a raw handle, or None for the device's current one.
+    (Handle 0 is the default stream; as an ExternalStream it would be a stream of the pool, 0 being "none given" there.)"""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    raw = int(getattr(stream, "cuda_stream", stream))
+    return torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+
+
 def _check(status: int, what: str):
     if status != QMM_OK:
         raise QmmError(status, what)

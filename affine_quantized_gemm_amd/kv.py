@@ -14,7 +14,7 @@ import math
 
 import torch
 
-from . import (_DT, _lib, QMM_ERR_UNSUPPORTED, QmmError, _check, _dev, _dt, _expect, _same_device)
+from . import (_DT, _as_stream, _lib, QMM_ERR_UNSUPPORTED, QmmError, _check, _dev, _dt, _expect, _same_device)
 
 _I32 = torch.int32
 ATTEND_ZEROED_BYTES = 65536  # QMM_KV_ATTEND_ZEROED_BYTES
@@ -131,8 +131,7 @@ class KVCache:
             return torch.empty_strided(shape, strides, dtype=dtype, device=self.device)
 
     def _as_stream(self, stream):
-        return stream if isinstance(stream, torch.cuda.Stream) else \
-            torch.cuda.ExternalStream(int(stream), device=self.device)
+        return _as_stream(stream, self.device)
 
     def _space(self, workspace, need, stream):
         if workspace is None:

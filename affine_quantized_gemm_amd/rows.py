@@ -13,7 +13,8 @@ from typing import NamedTuple
 
 import torch
 
-from . import (_DT, _lib, QMM_ERR_UNSUPPORTED, QmmError, _check, _check_quantized, _dev, _dt, _expect, _same_device)
+from . import (_DT, _as_stream, _lib, QMM_ERR_UNSUPPORTED, QmmError, _check, _check_quantized, _dev, _dt, _expect,
+               _same_device)
 
 ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}  # qmm_act
 PAIRS = {"halves": 0, "adjacent": 1}                      # qmm_pairs
@@ -56,8 +57,7 @@ class _On:
             return torch.empty(shape, dtype=dtype, device=self.device)
 
     def torch_stream(self):
-        return self.stream if isinstance(self.stream, torch.cuda.Stream) else \
-            torch.cuda.ExternalStream(self.raw, device=self.device)
+        return _as_stream(self.stream, self.device)
 
 
 def _fits(t, shape, dtype, index):
