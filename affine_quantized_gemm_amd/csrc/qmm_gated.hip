@@ -18,6 +18,14 @@ template <> DxFn dx_fn<DT_BF16, 4>(int);
 template <> DxFn dx_fn<DT_BF16, 6>(int);
 template <> DxFn dx_fn<DT_BF16, 8>(int);
 
+namespace {
+
+__global__ __launch_bounds__(256) void gated_dx_zero_kernel(uint4* y, int64_t n) {
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (at < n) y[at] = make_uint4(0, 0, 0, 0);
+}
+
+}  // namespace
 }  // namespace gated
 
 hipError_t launch_gated(const GatedArgs& a) {
@@ -122,6 +130,12 @@ hipError_t launch_gated_dx(const GatedArgs& a, void* y, float* part) {
     const hipError_t e = fn(p, static_cast<int>((a.M + 15) / 16), grid, a.stream);
     if (e != hipSuccess || plan.slices == 1) return e;
     return launch_reduce_partials(a.dt, part, y, plan.slices, a.M * a.K, a.stream);
+}
+
+hipError_t launch_gated_dx_zero(void* y, int64_t n, hipStream_t st) {
+    const dim3 grid(static_cast<unsigned>((n / 8 + 255) / 256));
+    hipLaunchKernelGGL(gated::gated_dx_zero_kernel, grid, dim3(256), 0, st, static_cast<uint4*>(y), n / 8);
+    return hipGetLastError();
 }
 
 }  // namespace qmm

@@ -103,5 +103,7 @@ struct GatedDxPlan {
 };
 GatedDxPlan gated_dx_plan(int64_t M, int64_t F, int64_t K);
 hipError_t launch_gated_dx(const GatedArgs& a, void* y, float* part);
+// n zeros of 2 bytes, a multiple of 8.
+hipError_t launch_gated_dx_zero(void* y, int64_t n, hipStream_t st);
 
 }  // namespace qmm

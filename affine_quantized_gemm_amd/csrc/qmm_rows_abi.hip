@@ -77,9 +77,13 @@ int qmm_gated_backward(int dt, int bits, int group_size, int act, int64_t M, int
     if (need < 0) return static_cast<int>(need);
     if (!known_act(act)) return QMM_ERR_UNSUPPORTED;
     if (workspace_bytes < 0) return QMM_ERR_INVALID_ARG;
-    if (M == 0 || F == 0) return QMM_OK;
-    int st = check_ptrs({x, wq, scales, biases, grad, grad_gate_up, grad_x}, 16);
-    if (st != QMM_OK) return st;
+    if (M == 0) return QMM_OK;
+    int st;
+    if (F == 0) {  // a sum of nothing
+        if ((st = check_ptrs({grad_x}, 16)) != QMM_OK) return st;
+        return hip_status(qmm::launch_gated_dx_zero(grad_x, M * K, static_cast<hipStream_t>(stream)));
+    }
+    if ((st = check_ptrs({x, wq, scales, biases, grad, grad_gate_up, grad_x}, 16)) != QMM_OK) return st;
     if (workspace == nullptr || workspace_bytes < need) return QMM_ERR_INVALID_ARG;
     if (off(workspace, 16)) return QMM_ERR_MISALIGNED;
     // the workspace: the two gradients in fp32, then the sums of grad_x's slices

@@ -151,9 +151,6 @@ def gated_backward(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor, bias
                                        None if workspace is None else workspace.data_ptr(),
                                        0 if workspace is None else workspace.numel() * workspace.element_size(), on.raw),
                "qmm_gated_backward")
-        if F == 0:
-            with torch.cuda.stream(on.torch_stream()):
-                out.zero_()
     return out, grad_gate_up
 
 

@@ -561,7 +561,8 @@ int qmm_gated(int dt, int bits, int group_size, int act, int64_t M, int64_t F, i
  *   grad_x [M, K]        = grad_gate_up . W
  * grad_gate_up is rounded once to dt; grad_x is formed from its fp32 values,
  * kept to 16 bits, and rounded once.  F a multiple of 16 (QMM_ERR_UNSUPPORTED
- * otherwise).
+ * otherwise); with F == 0 grad_x is zero and the only array looked at (M == 0:
+ * QMM_OK, nothing launched).
  * workspace: device memory of at least qmm_gated_backward_workspace_bytes(...)
  * bytes (a negative status for what is not supported), 16-byte aligned, not
  * aliasing the other arrays; two calls in flight need two.

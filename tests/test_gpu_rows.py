@@ -567,3 +567,13 @@ def test_gradient_of_no_columns_on_a_stream(Q):
         got = dx.clone()
     stream.synchronize()
     assert dx is out and dgu.shape == (3, 0) and not got.any()
+
+
+@pytest.mark.parametrize("rows,hidden", [(1, 64), (5, 192), (64, 4096)])
+def test_gradient_of_no_columns_from_c(Q, rows, hidden):
+    """The C entry writes grad_x of a block without columns itself, and nothing beside it."""
+    buffer = torch.full((rows + 1, hidden), 7.0, dtype=torch.bfloat16, device="cuda")
+    for _ in range(2):
+        status = Q._lib.qmm_gated_backward(1, 4, 64, 0, rows, 0, hidden, None, None, None, None, None, None, buffer.data_ptr(), None, 0,
+                                           torch.cuda.current_stream().cuda_stream)
+        assert status == Q.QMM_OK and not buffer[:rows].any() and (buffer[rows] == 7).all()

@@ -170,6 +170,13 @@ def test_gated_backward_refusals(kw, status):
     assert backward(**kw) == status
 
 
+@pytest.mark.parametrize("kw,status", [(dict(dx=None), INV), (dict(dx=MIS8), MIS), (dict(M=0, dx=None), OK)])
+def test_gated_backward_without_columns_refusals(kw, status):
+    """grad_x is written there too."""
+    none = dict(F=0, x=None, wq=None, s=None, b=None, grad=None, dgu=None, ws=None, bytes=0)
+    assert backward(**{**none, **kw}) == status
+
+
 def test_gated_backward_workspace():
     size = L.qmm_gated_backward_workspace_bytes
     need = size(0, 4, 64, 6, 2048, 4096)
