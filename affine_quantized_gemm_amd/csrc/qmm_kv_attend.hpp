@@ -65,6 +65,7 @@
 #include "qmm_device.hpp"
 #include "qmm_internal.hpp"
 #include "qmm_kv.hpp"
+#include "qmm_kv_window.hpp"
 #include "qmm_mfma_frag.hpp"
 
 namespace qmm {
@@ -227,60 +228,12 @@ struct Part {
     int b, part, parts, first, chunks, slot0;  // slot0: number of the sequence's first part
 };
 
-// With a window a sequence's steps are taken in another order, and those that
-// no row sees not at all: first the steps that all rows see whole (among the
-// sinks, then from where the last row's window surely begins to the new
-// tokens), then the others (the sinks' last, the window's begin, the new
-// ones).  So there is one loop for each form of a step, as without a window;
-// a branch in one loop, a third loop or a loop around two had up to 370
-// registers spilled.  Positions are counted in this order; each of the five
-// pieces lies `by` further on in the sequence.
-struct Window {
-    int len;         // tokens of all pieces
-    int all;         // of those that all rows see
-    int end[4], by[5];
-    __device__ __forceinline__ int real(int t) const {
-        return t + (t < end[0] ? by[0] : t < end[1] ? by[1] : t < end[2] ? by[2] : t < end[3] ? by[3] : by[4]);
-    }
-};
-__device__ __forceinline__ Window window_of(const NewTokens& nt, int64_t cap, int window, int sinks) {
-    auto down = [](int t) { return t & ~31; };
-    auto up = [](int t) { return (t + 31) & ~31; };
-    auto least = [](int x, int y) { return x < y ? x : y; };
-    auto most = [](int x, int y) { return x > y ? x : y; };
-    const int len = most(0, static_cast<int>(nt.pos0 + nt.n < cap ? nt.pos0 + nt.n : cap));
-    const int before = most(0, least(nt.pos0, len));
-    const int sinks_whole = down(least(sinks, before)), sinks_end = least(up(least(sinks, len)), len);
-    const int low = down(most(0, nt.pos0 - window));           // no row sees what is before it, and no sink
-    const int whole = most(up(most(0, nt.pos0 + nt.n - window)), sinks_whole);  // (a row sees at most nt.n new ones)
-    const int fresh = most(down(before), 0);
-    // pieces: begin and tokens
-    const bool some = whole < fresh;
-    const int n1 = some ? fresh - whole : 0;
-    const int n2 = some ? most(0, least(sinks_end, whole) - sinks_whole) : sinks_end - sinks_whole;
-    const int b3 = most(low, sinks_end), n3 = most(0, (some ? whole : len) - b3);
-    const int n4 = some ? len - fresh : 0;
-    Window w;
-    w.all = sinks_whole + n1;
-    w.end[0] = sinks_whole;
-    w.end[1] = w.all;
-    w.end[2] = w.all + n2;
-    w.end[3] = w.end[2] + n3;
-    w.len = w.end[3] + n4;
-    w.by[0] = 0;
-    w.by[1] = whole - w.end[0];
-    w.by[2] = sinks_whole - w.end[1];
-    w.by[3] = b3 - w.end[2];
-    w.by[4] = fresh - w.end[3];
-    return w;
-}
-
 // Every sequence gets ceil(chunks / T) parts with the least T (up to where
 // the search stops) for which they are at most `parts` together: all
 // workgroups then take about T chunks whatever the lengths are.  Each
 // workgroup finds the cut by itself from the lengths, 64 a register.
 template <bool WINDOW>
-__device__ __forceinline__ Part find_part(const Seqs& s, int unit, int parts, int lane, int window, int sinks) {
+__device__ __forceinline__ Part find_part(const Seqs& s, int unit, int parts, int lane, int window, int sinks, bool masked) {
     Part p;
     p.part = 0;
     p.parts = 1;
@@ -298,7 +251,10 @@ __device__ __forceinline__ Part find_part(const Seqs& s, int unit, int parts, in
         c[k] = 0;
         if (64 * k < s.seqs && b < s.seqs) {
             int64_t len = s.lens[b];
-            if constexpr (WINDOW) len = window_of(new_tokens(s, b), cap, window, sinks).len;
+            if constexpr (WINDOW) {
+                const NewTokens nt = new_tokens(s, b);
+                len = window_of(nt.pos0, nt.n, cap, window, sinks, masked).len;
+            }
             c[k] = static_cast<int>(((len < cap ? len : cap) + kChunk - 1) / kChunk);
             c[k] = c[k] > 0 ? c[k] : 1;
         }
@@ -1105,7 +1061,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
     // heads fastest; workgroups that read the same tokens (row groups, blockIdx.y) are a multiple of 8 apart: one XCD
     const uint32_t unit = blockIdx.x / static_cast<uint32_t>(a.s.kv_heads);
     const int head = static_cast<int>(blockIdx.x - unit * a.s.kv_heads), rg = blockIdx.y;
-    const Part part = find_part<WINDOW>(a.s, static_cast<int>(unit), a.parts, lane, a.window, a.sinks);
+    const Part part = find_part<WINDOW>(a.s, static_cast<int>(unit), a.parts, lane, a.window, a.sinks, a.mask != nullptr);
     const int b = part.b;
     if (b < 0) return;
     const NewTokens nt = new_tokens(a.s, b);
@@ -1115,7 +1071,7 @@ __global__ __launch_bounds__(64 * attend_waves(RT, ROWS), attend_occupancy(D, RT
     const int wave_row = base_row + (ROWS ? wave * 16 * RT : 0);  // the wavefront's first
     const int64_t cap = a.s.width << a.s.page_shift;
     Window win{};
-    if constexpr (WINDOW) win = window_of(nt, cap, a.window, a.sinks);
+    if constexpr (WINDOW) win = window_of(nt.pos0, nt.n, cap, a.window, a.sinks, a.mask != nullptr);
     const int len = WINDOW ? win.len : static_cast<int>(nt.pos0 + nt.n < cap ? nt.pos0 + nt.n : cap);
     // (positions are counted in the window's order up to where the record, or the place among the new tokens, counts)
     auto real = [&](int t) { return WINDOW ? win.real(t) : t; };

@@ -217,7 +217,8 @@ class KVCache:
         ones up to itself, or with ``mask`` (int64 [rows]) the new tokens j
         whose bit j its word has set.  A row that sees nothing gives zeros.
         With ``window``, of those tokens the last ``window`` and the ones at
-        positions below ``sinks``; pages of other tokens are not read.
+        positions below ``sinks``; pages of other tokens are not read (with
+        ``mask``: than those that a row whose word is 0 would see as well).
         ``scale`` defaults to 1/sqrt(head_dim).  ``max_len`` bounds the
         lengths for the split of the work (default: what the tables hold).
         ``workspace``: from :meth:`attend_workspace` (default: one that the

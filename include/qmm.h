@@ -464,8 +464,10 @@ int qmm_kv_attend(const qmm_kv_cache* cache, int layer, int64_t seqs, int64_t ma
  * `window` (1 or more) and besides those at positions below `sinks` (0 or
  * more).  A row of a draft tree thus has its own token, its ancestors and as
  * many tokens before the new ones as fill the window.  Tokens count whether
- * or not a page holds them.  Reads the pages of those tokens and no others:
- * table entries of pages that no row sees may be negative.
+ * or not a page holds them.  Reads the pages of those tokens and no others
+ * (with a mask: of the tokens that a row whose word is 0 would see as well,
+ * though none may be such a row): table entries of pages that no row sees may
+ * be negative.
  * The workspace is qmm_kv_attend's, at least
  * qmm_kv_attend_window_workspace_bytes(...) bytes (the same bound and
  * QMM_KV_ATTEND_ZEROED_BYTES hold; one workspace may serve both calls in

@@ -140,6 +140,31 @@ def test_pages_outside_the_window_are_not_read(Q):
     assert torch.equal(got.view(torch.int16), want.view(torch.int16))
 
 
+@pytest.mark.parametrize("dt,page,new", [("bf16", 64, 1), ("f16", 64, 6), ("bf16", 32, 4), ("f16", 32, 1)])
+def test_a_window_that_begins_with_a_page(Q, dt, page, new):
+    """The page before the first row's first token holds nothing that a row sees: NaN there has no part, bit for bit, and with
+    a mask, where the page is read, no more than another form of the steps has."""
+    lens = np.array([8 * page + new + 31, 5 * page + new + 12])
+    c, tables = filled(dt, 128, 64, page, 1, lens, 10, 20, 85)
+    mask = [(2 << i) - 1 for _ in lens for i in range(new)]
+    q = synth.normal((2 * new, 3, 128), 1.0, dt, 86).cuda()
+    for b in range(2):
+        window = int(lens[b] - new + 1) % page + page
+        first = int(lens[b]) - new + 1 - window  # of the first row
+        assert first % page == 0 and first > 0
+        want = check(Q, c, tables, lens, np.full(2, new), 3, 86, window, 2)
+        m = check(Q, c, tables, lens, np.full(2, new), 3, 86, window, 2, mask=mask)
+        kept = c["pool"].copy()
+        c["pool"][0, tables[b, first // page - 1]] = POISON
+        cache = gpu_cache(Q, c)
+        got = cache.attend(0, q, i32(tables), i32(lens), window=window, sinks=2)
+        assert torch.equal(got[b * new:(b + 1) * new].view(torch.int16), want[b * new:(b + 1) * new].view(torch.int16))
+        got = cache.attend(0, q, i32(tables), i32(lens), window=window, sinks=2, mask=torch.tensor(mask, device="cuda"))
+        step = 2.0 ** (-10 if dt == "f16" else -7)  # (another form of the steps: within two roundings)
+        assert ((got - m).float().abs() <= step * (m.float().abs() + 0.5))[b * new:(b + 1) * new].all()
+        c["pool"][...] = kept
+
+
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 def test_infinite_values_outside_the_window_have_no_part(Q, dt):
     """Tokens beside the window, in a step that is read for others, infinite or NaN: as if they were not there."""
