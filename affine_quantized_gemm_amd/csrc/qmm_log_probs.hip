@@ -626,6 +626,10 @@ __global__ __launch_bounds__(kThreads) void log_probs_grad_kernel(LogProbsGradAr
     }
 }
 
+constexpr int64_t kMostBlocks = UINT32_MAX / kThreads;  // of a launch: a grid's threads are 32 bits
+
+const void* after(const void* p, int64_t bytes) { return p != nullptr ? static_cast<const char*>(p) + bytes : nullptr; }
+
 }  // namespace
 
 // Parts of a row: for about kBlocks workgroups, each wavefront with a slice
@@ -648,32 +652,58 @@ hipError_t launch_log_probs(int dt, const LogProbsArgs& a, hipStream_t st) {
     p.part_vecs = (slices + p.parts - 1) / p.parts * kSlice;
     p.done = static_cast<uint32_t*>(a.workspace);
     p.sums = reinterpret_cast<uint64_t*>(static_cast<char*>(a.workspace) + QMM_LOG_PROBS_ZEROED_BYTES);
-    const int64_t blocks = a.rows * p.parts;
-    if (blocks > UINT32_MAX / kThreads) return hipErrorInvalidValue;  // (a grid's threads are 32 bits)
     int64_t words = static_cast<int64_t>(kWaves) * wave_keys(a.top) + a.top;
     if (p.parts > 1 && words < static_cast<int64_t>(p.parts) * a.top) words = static_cast<int64_t>(p.parts) * a.top;
-    const dim3 grid(static_cast<unsigned>(blocks));
     const unsigned bytes = static_cast<unsigned>(8 * words);
-    if (dt == DT_F16) {
-        if (a.top > 0) hipLaunchKernelGGL((log_probs_kernel<DT_F16, true>), grid, dim3(kThreads), bytes, st, p);
-        else hipLaunchKernelGGL((log_probs_kernel<DT_F16, false>), grid, dim3(kThreads), bytes, st, p);
-    } else {
-        if (a.top > 0) hipLaunchKernelGGL((log_probs_kernel<DT_BF16, true>), grid, dim3(kThreads), bytes, st, p);
-        else hipLaunchKernelGGL((log_probs_kernel<DT_BF16, false>), grid, dim3(kThreads), bytes, st, p);
+    for (int64_t row = 0; row < a.rows; row += kMostBlocks) {
+        const int64_t n = a.rows - row < kMostBlocks ? a.rows - row : kMostBlocks;
+        // (rows that are cut are few)
+        const dim3 grid(static_cast<unsigned>(n * p.parts));
+        p.a = a;
+        p.a.logits = static_cast<const uint16_t*>(a.logits) + row * a.stride;
+        p.a.tokens = after(a.tokens, row * a.given * (a.tokens64 ? 8 : 4));
+        p.a.lse = a.lse + row;
+        p.a.entropy = a.entropy + row;
+        if (a.given > 0) p.a.token_lp = a.token_lp + row * a.given;
+        if (a.top > 0) {
+            p.a.top_values = a.top_values + row * a.top;
+            p.a.top_ids = a.top_ids + row * a.top;
+        }
+        if (dt == DT_F16) {
+            if (a.top > 0) hipLaunchKernelGGL((log_probs_kernel<DT_F16, true>), grid, dim3(kThreads), bytes, st, p);
+            else hipLaunchKernelGGL((log_probs_kernel<DT_F16, false>), grid, dim3(kThreads), bytes, st, p);
+        } else {
+            if (a.top > 0) hipLaunchKernelGGL((log_probs_kernel<DT_BF16, true>), grid, dim3(kThreads), bytes, st, p);
+            else hipLaunchKernelGGL((log_probs_kernel<DT_BF16, false>), grid, dim3(kThreads), bytes, st, p);
+        }
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
-    return hipGetLastError();
+    return hipSuccess;
 }
 
 hipError_t launch_log_probs_grad(int dt, const LogProbsGradArgs& a, hipStream_t st) {
     const int64_t vecs = (a.vocab + 7) / 8 + 1;
     const int64_t blocks_row = (vecs + kGradVecs * kThreads - 1) / (kGradVecs * kThreads);
-    if (blocks_row * a.rows > UINT32_MAX / kThreads) return hipErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>(blocks_row * a.rows));
-    if (dt == DT_F16)
-        hipLaunchKernelGGL((log_probs_grad_kernel<DT_F16>), grid, dim3(kThreads), 0, st, a, static_cast<uint32_t>(blocks_row));
-    else
-        hipLaunchKernelGGL((log_probs_grad_kernel<DT_BF16>), grid, dim3(kThreads), 0, st, a, static_cast<uint32_t>(blocks_row));
-    return hipGetLastError();
+    const int64_t most = kMostBlocks / blocks_row;
+    for (int64_t row = 0; row < a.rows; row += most) {
+        const int64_t n = a.rows - row < most ? a.rows - row : most;
+        const dim3 grid(static_cast<unsigned>(blocks_row * n));
+        LogProbsGradArgs p = a;
+        p.logits = static_cast<const uint16_t*>(a.logits) + row * a.stride;
+        p.tokens = after(a.tokens, row * a.given * (a.tokens64 ? 8 : 4));
+        p.lse = a.lse + row;
+        if (a.entropy != nullptr) p.entropy = a.entropy + row;
+        if (a.grad_tokens != nullptr) p.grad_tokens = a.grad_tokens + row * a.given;
+        if (a.grad_entropy != nullptr) p.grad_entropy = a.grad_entropy + row;
+        if (a.grad_lse != nullptr) p.grad_lse = a.grad_lse + row;
+        p.out = static_cast<uint16_t*>(a.out) + row * a.out_stride;
+        if (dt == DT_F16)
+            hipLaunchKernelGGL((log_probs_grad_kernel<DT_F16>), grid, dim3(kThreads), 0, st, p, static_cast<uint32_t>(blocks_row));
+        else
+            hipLaunchKernelGGL((log_probs_grad_kernel<DT_BF16>), grid, dim3(kThreads), 0, st, p, static_cast<uint32_t>(blocks_row));
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace qmm

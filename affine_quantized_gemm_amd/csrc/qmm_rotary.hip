@@ -158,17 +158,24 @@ hipError_t launch_rotary(int dt, const RotaryArgs& a, hipStream_t st) {
     p.per_magic = magic_of(p.per);
     p.heads_magic = magic_of(p.head_block);
     const int64_t head_blocks = (a.heads + p.head_block - 1) / p.head_block;
-    // (a grid's threads are 32 bits on an axis)
-    if (row_blocks > UINT32_MAX / kThreads || head_blocks > 65535) return hipErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>(row_blocks), static_cast<unsigned>(head_blocks));
-    if (dt == DT_F16) {
-        if (a.adjacent) hipLaunchKernelGGL((rotary_kernel<DT_F16, true>), grid, dim3(kThreads), 0, st, p);
-        else hipLaunchKernelGGL((rotary_kernel<DT_F16, false>), grid, dim3(kThreads), 0, st, p);
-    } else {
-        if (a.adjacent) hipLaunchKernelGGL((rotary_kernel<DT_BF16, true>), grid, dim3(kThreads), 0, st, p);
-        else hipLaunchKernelGGL((rotary_kernel<DT_BF16, false>), grid, dim3(kThreads), 0, st, p);
+    if (head_blocks > 65535) return hipErrorInvalidValue;
+    const int64_t most = UINT32_MAX / kThreads * static_cast<int64_t>(p.row_block);  // rows of a launch: a grid's threads are 32 bits on an axis
+    for (int64_t row = 0; row < a.rows; row += most) {
+        p.a.rows = a.rows - row < most ? a.rows - row : most;
+        p.a.x = static_cast<const uint16_t*>(a.x) + row * a.x_row;
+        p.a.out = static_cast<uint16_t*>(a.out) + row * a.out_row;
+        p.a.pos = static_cast<const char*>(a.pos) + row * (a.pos64 ? 8 : 4);
+        const dim3 grid(static_cast<unsigned>((p.a.rows + p.row_block - 1) / p.row_block), static_cast<unsigned>(head_blocks));
+        if (dt == DT_F16) {
+            if (a.adjacent) hipLaunchKernelGGL((rotary_kernel<DT_F16, true>), grid, dim3(kThreads), 0, st, p);
+            else hipLaunchKernelGGL((rotary_kernel<DT_F16, false>), grid, dim3(kThreads), 0, st, p);
+        } else {
+            if (a.adjacent) hipLaunchKernelGGL((rotary_kernel<DT_BF16, true>), grid, dim3(kThreads), 0, st, p);
+            else hipLaunchKernelGGL((rotary_kernel<DT_BF16, false>), grid, dim3(kThreads), 0, st, p);
+        }
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
-    return hipGetLastError();
+    return hipSuccess;
 }
 
 }  // namespace qmm

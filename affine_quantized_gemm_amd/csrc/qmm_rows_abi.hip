@@ -142,7 +142,7 @@ int qmm_rotary(int dt, int64_t rows, int64_t heads, int64_t head_dim, int64_t ro
     return hip_status(qmm::launch_rotary(dt, a, static_cast<hipStream_t>(stream)));
 }
 
-// (rows and vocab up to 2^31: columns and rows of a grid are 32-bit)
+// (columns are 32-bit numbers; rows of more than a launch holds go in several)
 static int check_logits(int dt, int64_t rows, int64_t vocab, float scale, int64_t stride, int64_t given) {
     if (rows < 0 || vocab < 0 || stride < 0 || given < 0) return QMM_ERR_INVALID_ARG;
     if (!std::isfinite(scale) || scale <= 0.0f) return QMM_ERR_INVALID_ARG;

@@ -577,3 +577,50 @@ def test_gradient_of_no_columns_from_c(Q, rows, hidden):
         status = Q._lib.qmm_gated_backward(1, 4, 64, 0, rows, 0, hidden, None, None, None, None, None, None, buffer.data_ptr(), None, 0,
                                            torch.cuda.current_stream().cuda_stream)
         assert status == Q.QMM_OK and not buffer[:rows].any() and (buffer[rows] == 7).all()
+
+
+# ---- more rows than one launch holds (2^32 threads) ----
+
+BEYOND = (1 << 32) // 256 + 700  # workgroups of 256
+
+
+def test_log_probs_of_very_many_rows(Q):
+    """Two logits a row: around the end of the first launch and at the last rows as in calls of those rows alone."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    z = torch.randn(BEYOND, 2, generator=g, device="cuda").bfloat16()
+    t = torch.randint(-1, 3, (BEYOND,), generator=g, device="cuda")
+    gt, gh, gl = (torch.randn(BEYOND, generator=g, device="cuda") for _ in range(3))
+    print(f"log_probs {tuple(z.shape)}", flush=True)
+    r = Q.log_probs(z, t, top=1)
+    assert torch.equal(r.top_ids[:, 0], (z[:, 1] > z[:, 0]).long())
+    assert torch.allclose(r.lse, z.float().logsumexp(1), rtol=1e-5, atol=1e-5)
+    print("log_probs_backward", flush=True)
+    d = Q.log_probs_backward(z, t, r.lse, r.entropy, gt, grad_entropy=gh, grad_lse=gl)
+    for at in (slice(0, 1000), slice(BEYOND - 1500, BEYOND), slice(BEYOND // 2, BEYOND // 2 + 600)):
+        s = Q.log_probs(z[at], t[at], top=1)
+        assert all(torch.equal(a[at], b) for a, b in zip(r, s))
+        assert torch.equal(d[at], Q.log_probs_backward(z[at], t[at], s.lse, s.entropy, gt[at], grad_entropy=gh[at], grad_lse=gl[at]))
+
+
+def test_log_probs_gradient_of_very_many_workgroups(Q):
+    """Rows of two workgroups, one row of logits for all, int32 tokens."""
+    rows, vocab = BEYOND // 2 + 500, 4096
+    z = logits(1, vocab, "bf16", 2).expand(rows, vocab)
+    t = torch.randint(0, vocab, (rows, 2), dtype=torch.int32, device="cuda")
+    lse = z[:1].float().logsumexp(1).expand(rows).contiguous()
+    gt = torch.randn(rows, 2, device="cuda")
+    print(f"log_probs_backward {tuple(z.shape)}", flush=True)
+    d = Q.log_probs_backward(z, t, lse, None, gt)
+    for at in (slice(0, 100), slice(rows - 1000, rows)):
+        assert torch.equal(d[at], Q.log_probs_backward(z[at], t[at], lse[at], None, gt[at]))
+
+
+def test_rotary_of_very_many_rows(Q):
+    """A workgroup a row: 512 turned values of one head."""
+    x = synth.normal((1, 1, 512), 1.0, "f16", 97).cuda().expand(BEYOND, 1, 512)
+    pos = torch.randint(0, 1 << 20, (2, BEYOND), dtype=torch.int32, device="cuda")
+    freq = 10000.0 ** (-torch.arange(256, device="cuda") / 256)
+    print(f"rotary {tuple(x.shape)}", flush=True)
+    y = Q.rotary(x, pos, freq, sections=(100, 156))
+    for at in (slice(0, 100), slice(BEYOND - 1500, BEYOND)):
+        assert torch.equal(y[at], Q.rotary(x[at], pos[:, at].contiguous(), freq, sections=(100, 156)))
