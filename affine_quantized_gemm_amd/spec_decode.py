@@ -38,6 +38,8 @@ class Decoder:
     def __init__(self, layers=2, hidden=1024, heads=8, kv_heads=2, head_dim=128, ffn=2048, vocab=2048,
                  dtype=torch.bfloat16, cycle=13, habit=7.0, seed=0, window=None, sinks=0):
         self.layers, self.heads, self.kv_heads, self.head_dim, self.dtype = layers, heads, kv_heads, head_dim, dtype
+        if sinks and window is None:
+            raise ValueError("sinks need a window")
         self.window, self.sinks = window, sinks
         g = torch.Generator(device="cuda").manual_seed(seed)
         rand = lambda *shape: torch.randn(shape, generator=g, device="cuda")
@@ -208,6 +210,8 @@ def main(argv=None) -> None:
     a = p.parse_args(argv)
     if a.seqs * (1 + 2 * a.depth) > 64:
         p.error("seqs * (1 + 2 * depth) rows: at most 64")
+    if a.window < 0 or a.sinks < 0 or a.sinks and not a.window:
+        p.error("window and sinks: 0 or more, and sinks only with a window")
     model = Decoder(a.layers, a.hidden, a.heads, a.kv_heads, a.hidden // a.heads, a.ffn,
                     dtype=torch.float16 if a.dtype == "f16" else torch.bfloat16,
                     window=a.window or None, sinks=a.sinks)
