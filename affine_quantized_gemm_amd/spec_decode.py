@@ -95,6 +95,7 @@ class Sequences:
         self.said = torch.zeros(seqs, most_tokens + 64, device="cuda")     # the tokens' log probabilities (the first's is 0)
         self.tokens = torch.zeros(seqs, dtype=torch.int64, device="cuda")  # in the history; the last is not cached yet
         self.sound = torch.ones((), dtype=torch.int32, device="cuda")     # every page asked for was there
+        self.least = torch.zeros((), dtype=torch.int64, device="cuda")    # -1: a token was picked from NaN or infinite logits
         # the draft tree: rows 0, 1..depth and depth + 1..2 * depth, what each sees, and its two paths
         self.depth, branch = depth, range(1, depth + 1)
         self.level = torch.tensor([0, *branch, *branch], device="cuda")
@@ -131,7 +132,8 @@ class Sequences:
         self.history[1:], self.tokens[1:] = self.history[0].clone(), self.tokens[0].clone()
         self.said[1:] = self.said[0].clone()
         first = Q.log_probs(logits[None], top=seqs)
-        self.history.scatter_(1, self.tokens[:, None], first.top_ids.T)
+        self.least = torch.minimum(self.least, first.top_ids.min())
+        self.history.scatter_(1, self.tokens[:, None], first.top_ids.T.clamp(min=0))
         self.said.scatter_(1, self.tokens[:, None], first.top_values.T)
         self.tokens += 1
 
@@ -165,7 +167,9 @@ class Sequences:
             self.cache.append(layer, k[rows], v[rows], self.tables, self.lens)
         self.lens.copy_(start + kept + 1)
         places = self.tokens[:, None] + torch.arange(self.depth + 1, device="cuda")
-        self.history.scatter_(1, places, picks.gather(1, path))
+        taken = picks.gather(1, path)
+        self.least = torch.minimum(self.least, torch.where(places <= self.tokens[:, None] + kept[:, None], taken, 0).min())
+        self.history.scatter_(1, places, taken.clamp_(min=0))
         self.said.scatter_(1, places, said.gather(1, path))
         self.tokens += kept + 1
 
@@ -180,6 +184,7 @@ class Sequences:
     def texts(self) -> list[list[int]]:
         """Every sequence's tokens so far."""
         assert int(self.sound) == 1, "the cache has too few pages"
+        assert int(self.least) == 0, "a token's logits were NaN or infinite"
         return [row[:n] for row, n in zip(self.history.tolist(), self.tokens.tolist())]
 
     def scores(self) -> list[list[float]]:

@@ -555,6 +555,28 @@ def test_decoding_with_a_window(Q, dt):
         assert not torch.equal(S.logits_of(whole, text[:-1]).float()[60:], logits[60:])
 
 
+@pytest.mark.parametrize("when", ["fork", "step"])
+def test_decoding_of_nan_logits(Q, when):
+    """A token picked from NaN: no text is given out, and no index is outside the vocabulary meanwhile."""
+    from affine_quantized_gemm_amd import spec_decode as S
+    print(f"decoding of NaN logits, {when}", flush=True)
+    model = S.Decoder(layers=1, hidden=256, heads=2, kv_heads=1, head_dim=128, ffn=256, vocab=256)
+    s = S.Sequences(model, 2, 20 + 1 + 8 * 7, 3)
+    logits = s.prefill(torch.arange(20, device="cuda"))[-1]
+    if when == "fork":
+        logits = torch.full_like(logits, math.nan)
+    s.fork(logits)
+    if when == "step":
+        s.step()
+        assert all(len(t) >= 22 for t in s.texts())
+        model.head[1][7] = math.nan  # one column of scales' values
+    for _ in range(3):
+        s.step()
+        assert int(s.history.min()) >= 0 and int(s.history.max()) < 256
+    with pytest.raises(AssertionError, match="NaN or infinite"):
+        s.texts()
+
+
 def test_gradient_of_no_columns_on_a_stream(Q):
     """A block without columns: grad_x is zero, in the order of the stream that was given."""
     x = torch.ones(3, 64, dtype=torch.float16, device="cuda")
