@@ -104,8 +104,9 @@ __device__ __forceinline__ Act activation(int act, float a) {
         r.value = a * s;
         r.slope = s * (1.0f + a * (1.0f - s));
     } else if (act == ACT_RELU) {
-        r.value = fmaxf(a, 0.0f);
-        r.slope = a > 0.0f ? 1.0f : 0.0f;
+        // (NaN stays NaN)
+        r.value = a > 0.0f ? a : a != a ? a : 0.0f;
+        r.slope = a > 0.0f ? 1.0f : a != a ? a : 0.0f;
     } else if (act == ACT_GELU) {
         // half erfc of -a / sqrt 2: exact also where it is small
         const float phi = 0.5f * erfcf(-a * 0.707106781186547524f);

@@ -113,6 +113,22 @@ def test_gated_activations(Q, act, dt):
     check_gated(Q, dt, 8, 64, 6, 64, 256, 42, act=act, std=0.05, back=True)
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh", "relu"])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_gated_nan_in_the_gate(Q, act, dt):
+    """One column's gate is NaN by its weights, the other product's is not: h is NaN there, and both gradients and grad_x."""
+    x, _, (wq, sc, bi) = block(dt, 4, 64, 5, 32, 256, 43)
+    sc = sc.clone()
+    sc[9, 1] = math.nan
+    grad = synth.normal((5, 32), 1.0, dt, 44).cuda()
+    h = Q.gated(x.cuda(), wq, sc, bi, 4, 64, act=act)
+    dx, d = Q.gated_backward(x.cuda(), wq, sc, bi, 4, 64, grad, act=act)
+    at = torch.arange(32, device="cuda") == 9
+    assert torch.isnan(h[:, at]).all() and torch.isfinite(h[:, ~at]).all()
+    both = torch.cat([at, at])
+    assert torch.isnan(d[:, both]).all() and torch.isfinite(d[:, ~both]).all() and torch.isnan(dx).all()
+
+
 def test_gated_gradient_is_differences(Q):
     """grad_x of fp16 against differences of h itself, along random directions."""
     dt, rows, ffn, hidden = "f16", 4, 256, 512
