@@ -7,7 +7,7 @@
 //   lse = scale m + ln 2 log2 L,  H = ln 2 (log2 L - W / L),
 // in one pass: a lane keeps m, L and W of what it has seen and scales L and W
 // when its m moves (W then takes L times the move besides).  t of a barred
-// token (-infinity) is cut at -10^30, so that its product with 2^t is 0.
+// token (-infinity) is cut at -10^4, so that its product with 2^t is 0.
 //
 // The likeliest tokens: a logit's 16 bits as an ordered number and its column
 // make a key without equals (of equal logits the lowest column is first), so
@@ -49,7 +49,10 @@ constexpr int kMostParts = 64;                  // a lane each when they are joi
 constexpr int kBlocks = 1024;                   // workgroups that rows are cut for
 constexpr int kDoneStride = 32;                 // counters in lines of their own
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
-constexpr float kFarBelow = -1e30f;
+// What exponents are cut at where they multiply a power that is 0 there: far
+// beyond fp32's least, and small enough for finite products with sums of any
+// length and with incoming gradients.
+constexpr float kFarBelow = -1e4f;
 constexpr int kNothing = -32768;                // below every ordered logit that is a number
 constexpr int kFewLanes = 6;                    // whose values are put in one by one
 

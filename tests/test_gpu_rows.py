@@ -388,6 +388,22 @@ def test_log_probs_special_rows(Q):
             assert all(torch.equal(a[i], b[i]) for a, b in zip(r, c))
 
 
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 28, 2.0 ** 60, 2.0 ** 100])
+def test_log_probs_large_gradients_beside_barred_tokens(Q, size):
+    """Barred tokens and ones far below the others have no gradient, however large (a loss's scale) the entropy's is."""
+    z = logits(6, 1500, "bf16", 6, barred=0.3)
+    z[0, 1:] = -math.inf
+    z[1, 3:700] = -1e30
+    r = Q.log_probs(z)
+    g = np.random.default_rng(7)
+    gh, gl = (torch.from_numpy(size * g.normal(size=6)).float().cuda() for _ in range(2))
+    d, tol = RO.log_probs_backward(f64(z, "bf16"), None, r.lse.double().cpu().numpy(), r.entropy.double().cpu().numpy(), None,
+                                   gh.double().cpu().numpy(), gl.double().cpu().numpy(), 1.0, "bf16")
+    y = f64(Q.log_probs_backward(z, None, r.lse, r.entropy, None, grad_entropy=gh, grad_lse=gl), "bf16")
+    within(y, d, tol, f"gradient of size {size:.0e}")
+    assert not y[torch.isinf(z).cpu().numpy()].any()
+
+
 def test_log_probs_strides_and_alignment(Q):
     """Rows that begin anywhere, are spread out or one and the same; gradients into such rows, in place."""
     dt, vocab = "bf16", 2777
