@@ -533,8 +533,9 @@ __global__ __launch_bounds__(kThreads) void log_probs_kernel(Params p) {
     const bool bad = !(s.l == s.l) || s.m == __builtin_inff();
     const float nan = __builtin_nanf("");
     const float lse = bad ? nan : none ? -__builtin_inff() : __builtin_fmaf(ref, a.scale, kLn2 * log2_l);
+    // (halves: bf16 logits may lie further apart than fp32's largest)
     auto log_p = [&](float x) {
-        return bad ? nan : none || x == -__builtin_inff() ? -__builtin_inff() : kLn2 * __builtin_fmaf(x - ref, c, -log2_l);
+        return bad ? nan : none || x == -__builtin_inff() ? -__builtin_inff() : kLn2 * __builtin_fmaf(0.5f * x - 0.5f * ref, 2.0f * c, -log2_l);
     };
     if (threadIdx.x == 0) {
         a.lse[row] = lse;

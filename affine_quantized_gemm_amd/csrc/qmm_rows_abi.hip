@@ -146,6 +146,8 @@ int qmm_rotary(int dt, int64_t rows, int64_t heads, int64_t head_dim, int64_t ro
 static int check_logits(int dt, int64_t rows, int64_t vocab, float scale, int64_t stride, int64_t given) {
     if (rows < 0 || vocab < 0 || stride < 0 || given < 0) return QMM_ERR_INVALID_ARG;
     if (!std::isfinite(scale) || scale <= 0.0f) return QMM_ERR_INVALID_ARG;
+    // (within these, logits further apart than fp32's largest leave a probability of 0, and the scale in base 2 is finite)
+    if (scale < 0x1p-100f || scale > 0x1p100f) return QMM_ERR_UNSUPPORTED;
     if (!known_dt(dt) || given > 64 || rows > INT32_MAX || vocab > INT32_MAX - 1024) return QMM_ERR_UNSUPPORTED;
     return QMM_OK;
 }

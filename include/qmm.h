@@ -603,7 +603,8 @@ int qmm_rotary(int dt, int64_t rows, int64_t heads, int64_t head_dim, int64_t ro
 /*
  * Log probabilities of rows of logits [rows][vocab] (dt; row r at r * stride
  * elements, stride >= 0, any alignment of 2 bytes), z = scale * logit, scale
- * finite and above 0 (QMM_ERR_INVALID_ARG otherwise):
+ * finite and above 0 (QMM_ERR_INVALID_ARG otherwise), 2^-100 to 2^100
+ * (QMM_ERR_UNSUPPORTED otherwise):
  *   lse [rows]                 ln sum_v exp z_v
  *   entropy [rows]             -sum_v p_v ln p_v (nats), p_v = exp(z_v - lse)
  *   token_logprobs [rows][given]  z_t - lse of tokens [rows][given] (int32, or

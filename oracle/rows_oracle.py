@@ -149,7 +149,8 @@ def log_probs(logits, tokens, top, scale):
         total = np.exp(t).sum(1, keepdims=True)
         lse = np.where(none, -np.inf, m + np.log(total))
         p = np.where(none, 0, np.exp(t) / np.where(none, 1, total))
-        lp = np.where(none, -np.inf, z - lse)
+        # (not z - lse: beside logits of 10^37 the logarithm of the sum is below a step of 64 bits)
+        lp = np.where(none, -np.inf, t - np.log(total))
     size = np.where(np.isfinite(t), np.abs(t), 0)
     adds = 2.0 ** -24 * (vocab / 256 + 64)
     e = (p * 2.0 ** -23 * (8 + size)).sum(1) + adds

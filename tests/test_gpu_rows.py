@@ -404,6 +404,21 @@ def test_log_probs_large_gradients_beside_barred_tokens(Q, size):
     assert not y[torch.isinf(z).cpu().numpy()].any()
 
 
+@pytest.mark.parametrize("scale", [0.25, 2.0 ** -60, 2.0 ** -100, 2.0 ** 100])
+def test_log_probs_of_the_largest_differences(Q, scale):
+    """bf16 logits further apart than fp32's largest, whose scaled difference is not: finite log probabilities.  With the
+    largest scale, the smallest logits."""
+    size = 3e38 if scale < 1 else 2.0 ** -95
+    z = size * torch.randn(5, 700, generator=torch.Generator().manual_seed(8)).clamp_(-1, 1)
+    z[1] = -size
+    z[1, 9] = size
+    z[2, ::2] = -math.inf
+    z = z.bfloat16().cuda()
+    t = torch.arange(5, device="cuda") * 7 + 1
+    got = check_log_probs(Q, "bf16", z, t, 64, scale=scale, back=False)
+    assert torch.isfinite(got.tokens).all()
+
+
 def test_log_probs_strides_and_alignment(Q):
     """Rows that begin anywhere, are spread out or one and the same; gradients into such rows, in place."""
     dt, vocab = "bf16", 2777

@@ -86,6 +86,13 @@ def test_log_probs_oracle():
     assert r["top_ids"].tolist() == [[1, 0], [0, 1]]
 
 
+def test_log_probs_oracle_of_large_logits():
+    """Equal largest logits of any size: the same log probabilities."""
+    for size in (1.0, 1e20, 1e38):
+        r = RO.log_probs(size * np.array([[1.0, 1.0, 1.0, -1.0]]) - 60 * np.array([0, 0, 0, 1.0]), np.array([0]), 1, 1.0)
+        assert np.isclose(r["tokens"][0], -math.log(3)) and np.isclose(r["entropy"][0], math.log(3))
+
+
 def test_log_probs_gradient_is_differences():
     g = np.random.default_rng(1)
     z, tokens = g.normal(size=(4, 9)) * 2, np.array([[1, 1], [8, -100], [0, 3], [9, -1]])
@@ -230,6 +237,13 @@ def log_probs(**kw):
 ])
 def test_log_probs_refusals(kw, status):
     assert log_probs(**kw) == status
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -101, 2.0 ** 101, 3e38, 1e-44])
+def test_log_probs_scales_out_of_range(scale):
+    assert log_probs(scale=scale) == UNS and log_probs_backward(scale=scale) == UNS
+    assert log_probs(scale=scale, rows=0) == UNS
+    assert log_probs(scale=2.0 ** 100, rows=0) == OK and log_probs_backward(scale=2.0 ** -100, rows=0) == OK
 
 
 def test_log_probs_workspace_is_for_few_rows():
