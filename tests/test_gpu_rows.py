@@ -129,6 +129,25 @@ def test_gated_nan_in_the_gate(Q, act, dt):
     assert torch.isnan(d[:, both]).all() and torch.isfinite(d[:, ~both]).all() and torch.isnan(dx).all()
 
 
+@pytest.mark.parametrize("rows,hidden", [(5, 256), (5, 192), (40, 512), (64, 320)])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_gated_rows_keep_to_themselves(Q, dt, rows, hidden):
+    """A row of x or of the incoming gradient that is NaN or infinite has no part in the others, bit for bit."""
+    x, _, gpu = block(dt, 4, 32, rows, 48, hidden, 45)
+    x, grad = x.cuda(), synth.normal((rows, 48), 1.0, dt, 46).cuda()
+    others = torch.arange(rows, device="cuda") != 3
+    h, (dx, d) = Q.gated(x, *gpu, 4, 32), Q.gated_backward(x, *gpu, 4, 32, grad)
+    for bad in (math.nan, math.inf):
+        y, g = x.clone(), grad.clone()
+        y[3, 7] = bad
+        g[3, ::2] = bad
+        assert torch.equal(Q.gated(y, *gpu, 4, 32)[others], h[others])
+        for a, b in ((y, grad), (x, g)):
+            ex, ed = Q.gated_backward(a, *gpu, 4, 32, b)
+            assert torch.equal(ex[others], dx[others]) and torch.equal(ed[others], d[others])
+            assert not torch.isfinite(ex[3]).any()
+
+
 def test_gated_gradient_is_differences(Q):
     """grad_x of fp16 against differences of h itself, along random directions."""
     dt, rows, ffn, hidden = "f16", 4, 256, 512
@@ -693,3 +712,102 @@ def test_rotary_of_very_many_rows(Q):
     y = Q.rotary(x, pos, freq, sections=(100, 156))
     for at in (slice(0, 100), slice(BEYOND - 1500, BEYOND)):
         assert torch.equal(y[at], Q.rotary(x[at], pos[:, at].contiguous(), freq, sections=(100, 156)))
+
+
+# ---- the largest sizes that are taken ----
+
+@pytest.mark.parametrize("dt,bits,gs", [("bf16", 8, 64), ("f16", 4, 32), ("bf16", 6, 64)])
+@pytest.mark.parametrize("hidden", [1 << 24, (1 << 24) - 64 * 7])
+def test_gated_of_the_longest_rows(Q, dt, bits, gs, hidden):
+    """K of 2^24 and a little less (not of whole superblocks): rows of x that are zero but for a few places, so that products
+    are sums of a few weights; and the gradient's columns at both ends."""
+    rows, ffn = 64, 16
+    print(f"gated {dt} {bits}-bit gs={gs} K={hidden}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    wq = torch.randint(-2 ** 31, 2 ** 31 - 1, (2 * ffn, hidden * bits // 32), dtype=torch.int32, device="cuda", generator=g)
+    sc = (torch.rand(2 * ffn, hidden // gs, device="cuda", generator=g) / 2 ** bits).to(DT[dt])
+    bi = (torch.rand(2 * ffn, hidden // gs, device="cuda", generator=g) - 0.5).to(DT[dt])
+    places = torch.tensor([0, 63, 64, hidden // 2 + 5, hidden - 257, hidden - 64, hidden - 1], device="cuda")
+    x = torch.zeros(rows, hidden, dtype=DT[dt], device="cuda")
+    x[:, places] = torch.randn(rows, 7, device="cuda", generator=g).to(DT[dt])
+    w = Q.dequantize(wq, sc, bi, bits, gs)[:, places].double()  # (rounded to the type: 2^-8 or 2^-11 of each)
+    xs = x[:, places].double()
+    y, size = xs @ w.T, xs.abs() @ w.abs().T
+    gate, up = y[:, :ffn], y[:, ffn:]
+    want = torch.nn.functional.silu(gate) * up
+    # a weight's rounding, and fp32 sums of x (q + off) beside (b - off s) x: off s is at most 1024 * 2^-4 here
+    e = RO.UNIT[dt] * size + 2.0 ** -20 * xs.abs().sum(1, keepdim=True) * 64
+    tol = 1.2 * e[:, :ffn] * (up.abs() + e[:, ffn:]) + gate.abs() * e[:, ffn:] + 2 * RO.UNIT[dt] * want.abs() + 1e-6
+    h = Q.gated(x, wq, sc, bi, bits, gs)
+    assert ((h.double() - want).abs() <= tol).all()
+    for few in (slice(0, 5), slice(17, 40)):
+        assert ((Q.gated(x[few].contiguous(), wq, sc, bi, bits, gs).double() - want[few]).abs() <= tol[few]).all()
+    del w
+    grad = torch.randn(rows, ffn, device="cuda", generator=g).to(DT[dt])
+    dx, d = Q.gated_backward(x, wq, sc, bi, bits, gs, grad)
+    for at in (slice(0, 512), slice(hidden - 640, hidden)):
+        words, gr = slice(at.start * bits // 32, at.stop * bits // 32), slice(at.start // gs, at.stop // gs)
+        wd = Q.dequantize(wq[:, words].contiguous(), sc[:, gr].contiguous(), bi[:, gr].contiguous(), bits, gs).double()
+        ref, size = d.double() @ wd, d.double().abs() @ wd.abs()
+        assert ((dx[:, at].double() - ref).abs() <= 3 * RO.UNIT[dt] * size + 1e-6).all()
+
+
+def test_gated_of_very_many_columns(Q):
+    """40 million columns: offsets beyond 32 bits in the weights, the result and the gradients."""
+    ffn, hidden, rows = 40000016, 64, 33
+    g = torch.Generator(device="cuda").manual_seed(2)
+    wq = torch.randint(-2 ** 31, 2 ** 31 - 1, (2 * ffn, 8), dtype=torch.int32, device="cuda", generator=g)
+    sc = torch.rand(2 * ffn, 2, device="cuda", generator=g, dtype=torch.float32).div_(16).half()
+    bi = torch.rand(2 * ffn, 2, device="cuda", generator=g, dtype=torch.float32).sub_(0.5).half()
+    x = torch.randn(rows, hidden, device="cuda", generator=g).half()
+    print(f"gated F={ffn}", flush=True)
+    h = Q.gated(x, wq, sc, bi, 4, 32)
+    grad = torch.randn(rows, ffn, device="cuda", generator=g, dtype=torch.float16)
+    dx, d = Q.gated_backward(x, wq, sc, bi, 4, 32, grad)
+    for c in (0, ffn // 2 + 8, ffn - 1008):
+        at = torch.cat([torch.arange(c, c + 1008, device="cuda"), torch.arange(ffn + c, ffn + c + 1008, device="cuda")])
+        some = tuple(t[at].contiguous() for t in (wq, sc, bi))
+        # (another split of the same sums: within two roundings)
+        few = Q.gated(x, *some, 4, 32)
+        assert ((h[:, c:c + 1008] - few).float().abs() <= 2.0 ** -10 * few.float().abs() + 1e-4).all()
+        few = Q.gated_backward(x, *some, 4, 32, grad[:, c:c + 1008].contiguous())[1]
+        assert ((d[:, at] - few).float().abs() <= 2.0 ** -10 * few.float().abs() + 1e-4).all()
+    # grad_x as the sum over pieces of the columns, in 64 bits
+    ref, size = torch.zeros(rows, hidden, dtype=torch.float64, device="cuda"), torch.zeros(rows, hidden, dtype=torch.float64, device="cuda")
+    step = 2500000
+    for c in range(0, 2 * ffn, step):
+        wd = Q.dequantize(wq[c:c + step], sc[c:c + step], bi[c:c + step], 4, 32).double()
+        n = wd.shape[0] // 16  # (a long sum as 16 products)
+        p, wd = d[:, c:c + step].double().view(rows, 16, n).transpose(0, 1).contiguous(), wd.view(16, n, hidden)
+        ref, size = ref + (p @ wd).sum(0), size + (p.abs() @ wd.abs()).sum(0)
+    # d and the weights are rounded here, each by another amount, and sums are in fp32
+    assert ((dx.double() - ref).abs() <= 2.0 ** -11 * ref.abs() + 2.0 ** -16 * size + 1e-3).all()
+
+
+def test_log_probs_of_the_longest_rows(Q):
+    """1.5 billion logits: columns beyond 2^30, sums of as many equal terms."""
+    vocab = 1500000001
+    z = torch.zeros(1, vocab, dtype=torch.bfloat16, device="cuda")
+    t = torch.tensor([[0, vocab - 1, vocab, vocab // 2]], device="cuda")
+    print(f"log_probs of {vocab}", flush=True)
+    r = Q.log_probs(z, t, top=3)
+    assert r.top_ids.tolist() == [[0, 1, 2]]
+    for v in (r.lse, r.entropy, -r.tokens[0, 0], -r.tokens[0, 1], -r.top_values[0, 2]):
+        assert abs(float(v) - math.log(vocab)) < 1e-4
+    assert r.tokens[0, 2] == 0
+    z.fill_(-math.inf)
+    best = [vocab - 1, vocab - 2, 1 << 30, 12345]
+    z[0, best] = torch.tensor([3.0, 2.0, 1.0, 0.0], dtype=torch.bfloat16, device="cuda")
+    r = Q.log_probs(z, t, top=5)
+    assert r.top_ids.tolist() == [[*best, 0]]
+    want = torch.tensor([3.0, 2.0, 1.0, 0.0]).double().log_softmax(0)
+    assert np.allclose(r.top_values[0, :4].cpu().numpy(), want.numpy(), atol=1e-6) and r.top_values[0, 4] == -math.inf
+    assert abs(float(r.entropy) + float((want.exp() * want).sum())) < 1e-6
+    d = Q.log_probs_backward(z, t, r.lse, r.entropy, torch.ones(1, 4, device="cuda"))
+    assert d[0, vocab - 1].item() == pytest.approx(1 - 3 * math.exp(want[0]), rel=2.0 ** -8) and int((d != 0).sum()) == 6
+
+
+def test_log_probs_of_64_tokens(Q):
+    """As many given tokens as there may be, some of them the same, some padding; their gradient."""
+    for dt, rows, vocab in (("f16", 3, 5000), ("bf16", 70, 777)):
+        check_log_probs(Q, dt, logits(rows, vocab, dt, 9), some_tokens(rows, vocab, 64, 10), 64)
