@@ -46,6 +46,15 @@ hipError_t launch_gated(const GatedArgs& a) {
     p.groups = static_cast<int>(a.K / a.gs);
     const int super = super_of(a.bits);
     p.supers = static_cast<int>((a.K + super - 1) / super);
+    // Row tiles: a workgroup widens the codes once for all of its tiles, its other row blocks do it again.  4096 to 2 x
+    // 14336, us with one, two and four tiles: 4 bits (bf16, groups of 64) 16 rows 21 23 29, 17 rows 32 24 30, 32 rows 32 27
+    // 33, 33 rows 56 41 36, 64 rows 57 41 41; 6 bits (fp16, groups of 128) 16 rows 36 38 40, 17 rows 56 38 41, 33 rows 97 64
+    // 47, 64 rows 96 62 52; 8 bits alike.
+    // K not of whole superblocks: one tile and loads that are looked at one by one.  2 x 8192 columns, beside the next whole
+    // K: 4 bits, groups of 64, 6 rows of 2880 14.0 us and of 2816 11.7, 64 rows 24.9 and 31.2; groups of 32 (11 registers
+    // spilled) 6 rows of 896 8.9 and of 1024 6.7, of 1152 13.5 and of 1280 8.7, 64 rows of 896 18.2 and of 1024 16.6; 6 bits,
+    // 64 rows of 1088 17.7 and of 1152 17.2; 8 bits, 64 rows of 2880 29.5 and of 2816 26.0.  (The row blocks' second and
+    // later readings come from L2.)
     const bool vec = a.K % super == 0;
     const int rt = !vec || a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
     const int row_blocks = static_cast<int>((a.M + 16 * rt - 1) / (16 * rt));
@@ -93,7 +102,9 @@ hipError_t launch_gated(const GatedArgs& a) {
 }
 
 // Slices for the workgroups that the chip holds at a time: two a CU with one
-// row tile, else one.
+// row tile, else one.  (4 bits, 4096 to 2 x 14336, the whole call in us with 128,
+// 256, 512 and 1024 workgroups: 6 rows 68 49 48 52, 16 rows 70 52 51 56, 17 rows
+// 87 62 64 73, 37 rows 116 84 91 107, 64 rows 140 101 113 135.)
 GatedDxPlan gated_dx_plan(int64_t M, int64_t F, int64_t K) {
     using namespace gated;
     const int64_t blocks = (K + kDxCols - 1) / kDxCols, chunks = (2 * F + kDxRows - 1) / kDxRows;

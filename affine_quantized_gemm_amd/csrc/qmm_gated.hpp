@@ -28,11 +28,17 @@
 //
 // Measured (4 bits, groups of 64, unless said): 5 rows, 1024 to 2 x 2048, 5.0
 // us (start, one superblock or two, join; 0.3 of reading); 6 rows, 4096 to 2 x
-// 14336, 19.7 us (3.4 TB/s; 9.4 of reading: waits for the loads of few
-// wavefronts a SIMD, and start and join around them); 64 rows, 6 bits, groups
-// of 128, the same widths, 54 us (278 TFLOP/s; 13.4 of reading: the codes'
-// turning and widening for each of 16 columns, once for all row tiles, and the
-// matrix steps wait for one another's LDS); with a gradient, 37 rows, 39.5 us.
+// 14336, 19.5 us (3.4 TB/s; 9.4 of reading).  There 224 workgroups of 16
+// wavefronts at 127 registers and 136 KB of LDS fill a CU each, 32 CUs are left
+// empty, and a wavefront takes 4 superblocks in all, two of them on their way
+// and each turned in LDS: 43 % of the wavefronts' time is waiting for data or a
+// barrier, 36 % for a unit.  (The register kernel of the plain product reads the
+// same bytes as two products of 14336 columns in 16.3 us.)  64 rows, 6 bits,
+// groups of 128, the same widths, 54 us (278 TFLOP/s; 13.4 of reading): x of 64
+// rows goes through LDS in 8 chunks with two barriers around each, and two
+// wavefronts a SIMD, 207 registers, turn and widen the codes in between; vector
+// units busy 36 % of the time, matrix cores 10 %, 37 % of LDS's busy cycles are
+// conflicts.  With a gradient, 37 rows, 4 bits, 39.5 us (30 %, 16 %, 28 %).
 #pragma once
 
 #include "qmm_device.hpp"
@@ -99,7 +105,7 @@ __device__ __forceinline__ Act activation(int act, float a) {
     constexpr float log2e = 1.44269504088896341f;
     Act r;
     if (act == ACT_SILU) {
-        // (a far below 0: exp is infinite, s and r 0; infinite times 0 does not arise, a is finite)
+        // (a far below 0: exp is infinite, s and r 0; an infinite a gives NaN where it meets that 0)
         const float s = 1.0f / (1.0f + __builtin_amdgcn_exp2f(-a * log2e));
         r.value = a * s;
         r.slope = s * (1.0f + a * (1.0f - s));

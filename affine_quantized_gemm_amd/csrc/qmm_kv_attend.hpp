@@ -1037,7 +1037,8 @@ __device__ __forceinline__ void join_parts(Shared sums, uint32_t at0, uint32_t s
 // of 13 rows, 16 heads of 64, up to 2k 12.6 us.  With a window: of 4096 and 4
 // sinks, one token at 131071, 13.9 us; of 1023 and 4, 16 sequences of 4..6 rows
 // near 8k, 22 us; of 4096 and 64, 64 rows of 4 sequences near 16k, 48 us (366
-// TFLOP/s; 14; 43 in a row of calls).  A call starts (lengths, plan,
+// TFLOP/s; 14; 43 in a row of calls): an eighth to a sixth more than over as many
+// tokens without one (qmm_kv_window.hpp).  A call starts (lengths, plan,
 // q, page ids, first tokens) in 3 to 4 us and joins its parts in about 4;
 // between them one row tile is bound by its reads (6 TB/s over 131071 tokens).
 // With two no unit is full: vector ALUs 52 % busy (verify rows) and 63 % (64

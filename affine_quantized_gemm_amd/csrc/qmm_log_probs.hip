@@ -19,10 +19,16 @@
 // are put in one by one (a comparison, a count of lanes and a shift by a lane).
 // Of a slice with many no more is collected, in LDS, than what is at or above
 // the top-th of the lanes' largest: at most 16 values of `top` lanes, whatever
-// the values are.  (1000 rows of 152k, fp16: none likeliest 64 us, 1 78, 5 96,
-// 20 112, 64 464.  The 20 took 163 us without the first way and the others'
-// keys, 128 without their (top / 4)-th.)  What bounds it is the vector units'
-// work a logit: the exponential, t's cut and the two sums, 64 us of it.
+// the values are.  (1000 rows of 152k, fp16 and bf16: none likeliest 63 and 60
+// us, 1 79 and 78, 5 114 and 101, 20 half barred 112, all there 127 and 120, 48
+// 136 and 151, 63 168 and 207, 64 463 and 633.  The 20 half barred took 163 us
+// without the first way and the others' keys, 128 without their (top / 4)-th.)
+// Of 64 likeliest the 64 lanes' largest bound nothing: a wavefront collects all
+// 1024 values of its first slice and ranks each among all of them, which is the
+// 290 to 430 us between 63 and 64.  Besides that the vector units' work a logit
+// bounds it (the exponential, t's cut and the two sums; with 20 likeliest they
+// are busy 72 % of the time): 60 us of it.  The bf16 form has 132 registers,
+// three wavefronts a SIMD; fp16's 120 leave room for four.
 //
 // A row is one workgroup's, or cut into parts of whole slices where rows are
 // few; the workgroup that is last to finish a row joins the parts.
@@ -46,7 +52,11 @@ constexpr int kVecs = 2;                        // 16-byte pieces of a lane in a
 constexpr int kSlice = 64 * kVecs;              // pieces
 constexpr int kMostTop = QMM_LOG_PROBS_MOST_TOP;
 constexpr int kMostParts = 64;                  // a lane each when they are joined
-constexpr int kBlocks = 1024;                   // workgroups that rows are cut for
+// Workgroups that rows are cut for (152k logits, one likeliest, bf16; with 512:
+// 300 rows 36 us and 43, 6 rows 11.0 with 8 likeliest either way, but 28 rows 17
+// and 13, 64 rows 21 and 16, where the joining of twice the parts costs more
+// than the emptier chip).
+constexpr int kBlocks = 1024;
 constexpr int kDoneStride = 32;                 // counters in lines of their own
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 // What exponents are cut at where they multiply a power that is 0 there: far
@@ -54,7 +64,9 @@ constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 // length and with incoming gradients.
 constexpr float kFarBelow = -1e4f;
 constexpr int kNothing = -32768;                // below every ordered logit that is a number
-constexpr int kFewLanes = 6;                    // whose values are put in one by one
+// Lanes whose values are put in one by one (1000 rows, 20 likeliest, fp16 and
+// bf16: 2 to 8 lanes 104 to 107 us and 120 to 122, 16 109 and 124, none 114 and 147).
+constexpr int kFewLanes = 6;
 
 // 64-bit words of a part: m and L, W, then its keys.
 constexpr int part_words(int top) { return 2 + top; }

@@ -3,6 +3,8 @@
 Argument checks and marshalling only; every step runs in the HIP kernels of
 ``libqmm.so`` (``qmm_gated``, ``qmm_rotary``, ``qmm_log_probs`` and the
 gradients in ``include/qmm.h``, where the formulas and contracts are).
+None of them records itself for torch's autograd: the ``_backward`` calls (and
+``rotary`` with ``inverse``) are the gradients.
 """
 
 from __future__ import annotations

@@ -642,7 +642,8 @@ int qmm_log_probs(int dt, int64_t rows, int64_t vocab, float scale, const void* 
  * elements, out_stride >= vocab).  Each of the three may be NULL (entropy too
  * without grad_entropy).  A token named twice counts twice; padding has no
  * part.  Rows whose lse is -infinity get zeros.  out may be logits with the
- * same stride.
+ * same stride.  Probabilities are exp(z_v - lse), so that they share the fp32
+ * rounding of z and lse: within 2^-23 (|z_v| + |lse|) of themselves.
  */
 int qmm_log_probs_backward(int dt, int64_t rows, int64_t vocab, float scale, const void* logits, int64_t stride,
                            const void* tokens, int tokens_64, int64_t given, const float* lse, const float* entropy,
