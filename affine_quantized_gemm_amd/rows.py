@@ -289,7 +289,7 @@ def log_probs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top: int
     ``tokens`` [rows] or [rows, n] (int32 or int64; an id outside the
     vocabulary, padding, gets 0); ``top``: so many of the likeliest tokens (up
     to 64), of equal logits the lowest id first.  ``scale`` is the inverse
-    temperature.  ``workspace``: from :func:`log_probs_workspace` (default: one
+    temperature (2^-100 to 2^100).  ``workspace``: from :func:`log_probs_workspace` (default: one
     kept for the stream)."""
     dt, rows, vocab, stride, given = _check_logits(logits, tokens, scale)
     if not 0 <= top <= min(64, vocab):
